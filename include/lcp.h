@@ -48,7 +48,7 @@
 extern "C" {
 #endif
 
-#define LCP_ABI_VERSION 4
+#define LCP_ABI_VERSION 5
 
 #if defined(__GNUC__)
 #define LCP_API __attribute__((visibility("default")))
@@ -222,6 +222,64 @@ LCP_API lcp_status lcp_train(const lcp_layer* layers, int nlayers, const lcp_hpa
                              int count, int total, float tau_start, float tau_end, void* ws,
                              size_t ws_bytes, cudaStream_t stream);
 
+/* ---- Gradient norm, clipping and the update of many tensors ("Implementation
+ * details" trains every layer of a model with AdamW; clipping by the norm over
+ * all of its gradients is the library's extension).
+ *
+ * norm is the 2-norm over every value of every tensor of the list, summed in
+ * float64 in a fixed order, and the clipping factor is
+ *   f = min(1, max_norm / (norm + 1e-6)).
+ * A norm that is not finite is passed on: NaN makes the factor NaN, infinity
+ * makes it 0 (a gradient that is itself infinite or NaN then becomes NaN).
+ * Tensors of one list must not overlap each other (not checked here; the
+ * Python lists check it).  Any length from 0 on and any alignment to the
+ * element type are taken; 16-byte aligned tensors run fastest.  `ws` is a
+ * device buffer of at least lcp_clip_workspace_size() bytes, 256-byte aligned,
+ * that needs no preparation and is not used by an overlapping call.  The lists
+ * and their count are host data, read before the call returns. */
+typedef struct {
+  const void* g;     /* in  n gradient values in `dtype`                                  */
+  void* out;         /* out n values, f g rounded to `dtype`; may equal g (in place)      */
+  long long n;
+  lcp_dtype dtype;
+} lcp_grad;
+
+typedef struct {
+  float* L;          /* in/out n parameters                                               */
+  const float* dL;   /* in     n gradient values                                          */
+  float* m;          /* in/out first moments                                              */
+  float* v;          /* in/out second moments                                             */
+  long long n;
+} lcp_adamw_tensor;
+
+/* ("Implementation details") Bytes of workspace the three calls below need for `count` tensors. */
+LCP_API lcp_status lcp_clip_workspace_size(int count, size_t* bytes);
+
+/* ("Implementation details") norm[0] = the 2-norm over the list (float32; 0 for an empty list).  grads[i].out is not used. */
+LCP_API lcp_status lcp_grad_norm(const lcp_grad* grads, int count, float* norm, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream);
+
+/* ("Implementation details") norm[0] = the 2-norm over the list and out = f g for every tensor.  max_norm > 0
+ * (infinity: the gradients are copied unclipped). */
+LCP_API lcp_status lcp_grad_clip(const lcp_grad* grads, int count, double max_norm, float* norm, void* ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+
+/* ("Implementation details": AdamW on the logits) norm[0] = the 2-norm over the list's gradients and lcp_adamw's update of
+ * every tensor with f dL as its gradient; dL itself is left as it is.  max_norm > 0 (infinity: no clipping).
+ * t >= 1. */
+LCP_API lcp_status lcp_adamw_list(const lcp_adamw_tensor* tensors, int count, const lcp_adamw_params* opt, int t,
+                                  double max_norm, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ("Implementation details") lcp_train with the gradients of all layers clipped together: each
+ * step ends with one lcp_adamw_list over the layers' logits instead of an
+ * lcp_adamw a layer.  norm[0] receives the last step's norm over all dL (before
+ * clipping; dL holds the unclipped gradients).  ws: at least the larger of
+ * lcp_workspace_size() and lcp_clip_workspace_size(nlayers). */
+LCP_API lcp_status lcp_train_clip(const lcp_layer* layers, int nlayers, const lcp_hparams* hp,
+                                  const lcp_adamw_params* opt, const lcp_adamw_state* state, int first, int count,
+                                  int total, float tau_start, float tau_end, double max_norm, float* norm, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
 /* Importance scores of W for the mask ("integration with existing pruning
  * methods"; the pages name Wanda and RIA without defining them, so their
  * published definitions are used), with ||X_j|| the 2-norm of input channel j
@@ -359,6 +417,51 @@ LCP_API lcp_status lcp_gather(const void* X, const int32_t* perm, void* Xp, int 
 LCP_API lcp_status lcp_sparse24_mm(const void* values, const uint32_t* meta, const void* X, const int32_t* perm,
                                    float* Y, int cout, int cin, int tokens, int B, lcp_dtype dtype,
                                    cudaStream_t stream);
+
+/* ---- 8-bit deployment ("Effect on inference acceleration": the deployed layer
+ * at run time; 8-bit storage is the library's extension).  The weight A =
+ * M.(W P_B) of any N:M pattern, or an unpruned W, is stored densely as e4m3
+ * values with one power-of-two scale for each block of 128 x 128, and the
+ * activations as e4m3 values with one scale for each token and 128 channels.
+ * Scales are e8m0 bytes: byte e stands for 2^(e - 127), 255 for NaN.
+ *
+ * Quantisation: with amax the largest magnitude of a block, its scale is 2^k, k
+ * the smallest integer >= -127 with amax <= 448 2^k (k = 0 for a block of
+ * zeros), and q = x 2^-k rounded to the nearest e4m3 value, ties to even.  A
+ * block that holds an infinity or a NaN gets the NaN scale and NaN values, and
+ * so does every output it enters.
+ *
+ * G = ceil(C_in / 128) groups of channels; a last group or block that is not
+ * whole holds what there is.  C_in a multiple of 32; with perm also of B, B in
+ * {32, 64, 128, 256}.  perm as for lcp_gather; an entry outside [0, B) is
+ * skipped and recorded in lcp_device_error (302), and like any perm that is not
+ * a permutation of its block leaves unspecified values.  Outputs must not
+ * overlap inputs. */
+
+/* ("Effect on inference acceleration": the run-time channel permutation) Activations: Q [T, C_in] e4m3 and S [T, G] e8m0 of x_pi (perm NULL: of x) for
+ * X [T, C_in] in `dtype`.  T = 0 is a no-op. */
+LCP_API lcp_status lcp_quant8(const void* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B,
+                              lcp_dtype dtype, cudaStream_t stream);
+
+/* ("Effect on inference acceleration": the stored weight) Q [C_out, C_in] e4m3 and S [ceil(C_out/128), G] e8m0 of
+ * A = M.(W P_B) for W [C_out, C_in] in `dtype` (original column order), perm (NULL: identity) and the mask bits of M
+ * [C_out, C_in/32] in permuted order (NULL: keep everything).  A pruned entry is zero whatever W holds there. */
+LCP_API lcp_status lcp_quant8_weight(const void* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S,
+                                     int cout, int cin, int B, lcp_dtype dtype, cudaStream_t stream);
+
+/* ("Effect on inference acceleration": the deployed product) Y [T, C_out] = X W^T of 8-bit operands, Xq [T, C_in] with
+ * Xs [T, G] and Wq [C_out, C_in] with Ws [ceil(C_out/128), G]; products and sums in float32 on the tensor cores, Y
+ * rounded to `ydtype` once.  T = 0 is a no-op. */
+LCP_API lcp_status lcp_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, void* Y, int cout,
+                           int cin, int tokens, lcp_dtype ydtype, cudaStream_t stream);
+
+/* ("Effect on inference acceleration": the permuted layer at run time) lcp_quant8 of X and lcp_mm8 with the result: the
+ * 8-bit layer on activations X [T, C_in] in `dtype`, original channel order when perm is given.  ws: a device buffer of at
+ * least lcp_linear8_workspace_size() bytes, 256-byte aligned, not used by an overlapping call. */
+LCP_API lcp_status lcp_linear8_workspace_size(int tokens, int cin, size_t* bytes);
+LCP_API lcp_status lcp_linear8(const uint8_t* Wq, const uint8_t* Ws, const void* X, const int32_t* perm, void* Y,
+                               int cout, int cin, int tokens, int B, lcp_dtype dtype, lcp_dtype ydtype, void* ws,
+                               size_t ws_bytes, cudaStream_t stream);
 
 /* Diagnostic (synchronous: reads a device word).  Every wait inside the
  * tensor-core kernels is bounded; a wait that expires records its site here

@@ -50,6 +50,14 @@ class LcpAdamwState(ctypes.Structure):
     _fields_ = [("m", _c_void_p), ("v", _c_void_p)]
 
 
+class LcpGrad(ctypes.Structure):
+    _fields_ = [("g", _c_void_p), ("out", _c_void_p), ("n", ctypes.c_longlong), ("dtype", _c_int)]
+
+
+class LcpAdamwTensor(ctypes.Structure):
+    _fields_ = [("L", _c_void_p), ("dL", _c_void_p), ("m", _c_void_p), ("v", _c_void_p), ("n", ctypes.c_longlong)]
+
+
 class LcpError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(msg)
@@ -103,6 +111,23 @@ def lib() -> ctypes.CDLL:
                        _c_void_p], _c_int),
         "lcp_train": ([P(LcpLayer), _c_int, P(LcpHparams), P(LcpAdamwParams), P(LcpAdamwState), _c_int, _c_int,
                        _c_int, _c_float, _c_float, _c_void_p, ctypes.c_size_t, _c_void_p], _c_int),
+        "lcp_clip_workspace_size": ([_c_int, P(ctypes.c_size_t)], _c_int),
+        "lcp_grad_norm": ([P(LcpGrad), _c_int, _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p], _c_int),
+        "lcp_grad_clip": ([P(LcpGrad), _c_int, ctypes.c_double, _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p],
+                          _c_int),
+        "lcp_adamw_list": ([P(LcpAdamwTensor), _c_int, P(LcpAdamwParams), _c_int, ctypes.c_double, _c_void_p,
+                            _c_void_p, ctypes.c_size_t, _c_void_p], _c_int),
+        "lcp_train_clip": ([P(LcpLayer), _c_int, P(LcpHparams), P(LcpAdamwParams), P(LcpAdamwState), _c_int, _c_int,
+                            _c_int, _c_float, _c_float, ctypes.c_double, _c_void_p, _c_void_p, ctypes.c_size_t,
+                            _c_void_p], _c_int),
+        "lcp_quant8": ([_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p], _c_int),
+        "lcp_quant8_weight": ([_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                               _c_void_p], _c_int),
+        "lcp_mm8": ([_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p],
+                    _c_int),
+        "lcp_linear8_workspace_size": ([_c_int, _c_int, P(ctypes.c_size_t)], _c_int),
+        "lcp_linear8": ([_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int,
+                         _c_int, _c_void_p, ctypes.c_size_t, _c_void_p], _c_int),
         "lcp_selftest_bounded_wait": ([P(_c_int)], _c_int),
         "lcp_pack24": ([_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
                         _c_void_p], _c_int),
@@ -147,6 +172,24 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name: str = "") -> Optional[int]
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+class _on_device:
+    """Makes a device current for a call and restores the caller's (nothing to do on the current one)."""
+
+    def __init__(self, device: torch.device):
+        self.index, self.prev = device.index, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.index:
+            self.prev = cur
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+        return False
 
 
 def hparams(block: int, n: int, m: int, iters: int, tau: float, dtype: int, flags: int = 0) -> LcpHparams:
@@ -232,21 +275,130 @@ def adamw(L: torch.Tensor, dL: torch.Tensor, m: torch.Tensor, v: torch.Tensor, o
                           _ptr(v, torch.float32, "v"), L.numel(), ctypes.byref(opt), t, _stream(None)))
 
 
+def _check_disjoint(spans) -> None:
+    """Raises when two (address, bytes) ranges overlap."""
+    spans = sorted(s for s in spans if s[1])
+    for (a, n), (b_, _) in zip(spans, spans[1:]):
+        if a + n > b_:
+            raise ValueError("tensors of one list must not overlap")
+
+
+def _list_device(tensors) -> torch.device:
+    """The one CUDA device of a list of tensors (the current one for an empty list)."""
+    devs = {t.device for t in tensors}
+    if len(devs) > 1:
+        raise ValueError("tensors of one list must be on one device")
+    return devs.pop() if devs else torch.device("cuda", torch.cuda.current_device())
+
+
+class _TensorList:
+    """The norm and workspace buffers of a prepared list, allocated once; a call runs on the list's device."""
+
+    def _prepare(self, count: int, device: torch.device) -> None:
+        nbytes = ctypes.c_size_t(0)
+        check(lib().lcp_clip_workspace_size(count, ctypes.byref(nbytes)))
+        self.n = count
+        self.device = device
+        self.ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8, device=device)
+        self.norm_out = torch.empty(1, dtype=torch.float32, device=device)
+
+    def _call(self, fn, *args, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+        tail = (self.norm_out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        with _on_device(self.device):
+            check(fn(self.arr, self.n, *args, *tail, _stream(stream)))
+        return self.norm_out
+
+
+class GradList(_TensorList):
+    """A prepared list of gradient tensors (float32 or bf16, mixed, any sizes): ``norm()``
+    enqueues their common 2-norm, ``clip(max_norm)`` the norm and ``out = g * min(1, max_norm /
+    (norm + 1e-6))`` for every tensor (``out`` None: in place).  Both return the norm, one
+    float32 on the device that the next call on this list overwrites.  Calls on one list share
+    its workspace: do not run them on two streams at once."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError("one output per gradient")
+        device = _list_device(self.grads + self.out)
+        items, spans = [], []
+        for g, o in zip(self.grads, self.out):
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError("an output has the dtype and shape of its gradient")
+            p, q, size = _ptr(g, None, "grad"), _ptr(o, None, "out"), g.numel() * g.element_size()
+            items.append(LcpGrad(p, q, g.numel(), _dt(g)))
+            spans += [(p, size)] if p == q else [(p, size), (q, size)]
+        _check_disjoint(spans)
+        self.arr = (LcpGrad * max(1, len(items)))(*items)
+        self._prepare(len(items), device)
+
+    def norm(self, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        return self._call(lib().lcp_grad_norm, stream=stream)
+
+    def clip(self, max_norm: float, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        return self._call(lib().lcp_grad_clip, float(max_norm), stream=stream)
+
+
+class AdamwList(_TensorList):
+    """A prepared list of float32 parameters with their gradients and moments: ``run(opt, t,
+    max_norm)`` enqueues one AdamW update of all of them, the gradients clipped by their common
+    norm (the default leaves them unclipped), and returns that norm as ``GradList`` does."""
+
+    def __init__(self, L: Sequence[torch.Tensor], dL: Sequence[torch.Tensor], m: Sequence[torch.Tensor],
+                 v: Sequence[torch.Tensor]):
+        self.tensors = [list(L), list(dL), list(m), list(v)]
+        if len({len(x) for x in self.tensors}) != 1:
+            raise ValueError("L, dL, m and v must be lists of one length")
+        device = _list_device([t for x in self.tensors for t in x])
+        items, spans = [], []
+        for group in zip(*self.tensors):
+            if len({t.numel() for t in group}) != 1:
+                raise ValueError("a parameter, its gradient and its moments have one size")
+            ptrs = [_ptr(t, torch.float32, name) for t, name in zip(group, ("L", "dL", "m", "v"))]
+            items.append(LcpAdamwTensor(*ptrs, group[0].numel()))
+            spans += [(p, 4 * group[0].numel()) for p in ptrs]
+        _check_disjoint(spans)
+        self.arr = (LcpAdamwTensor * max(1, len(items)))(*items)
+        self._prepare(len(items), device)
+
+    def run(self, opt: LcpAdamwParams, t: int, max_norm: float = float("inf"),
+            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        return self._call(lib().lcp_adamw_list, ctypes.byref(opt), t, float(max_norm), stream=stream)
+
+
 class Trainer:
     """AdamW training of the logits of prepared layers (lcp_train): ``run(first,
     count)`` enqueues steps first .. first + count - 1 of a ``total``-step run
-    with the temperature going linearly from ``tau_start`` to ``tau_end``."""
+    with the temperature going linearly from ``tau_start`` to ``tau_end``.
+    With ``max_norm`` every step clips the gradients of all layers by their
+    common norm (lcp_train_clip); ``grad_norm`` (one float32 on the device)
+    then holds the last step's norm."""
 
     def __init__(self, step: "Step", opt: LcpAdamwParams, total: int, tau_start: float = 1.0,
-                 tau_end: float = 0.1):
+                 tau_end: float = 0.1, max_norm: Optional[float] = None):
         self.step, self.opt, self.total = step, opt, total
         self.tau_start, self.tau_end = tau_start, tau_end
         self.moments = [(torch.zeros_like(d["L"]), torch.zeros_like(d["L"])) for d in step.layers]
         self.state = (LcpAdamwState * len(self.moments))(*[LcpAdamwState(m.data_ptr(), v.data_ptr())
                                                            for m, v in self.moments])
+        self.max_norm, self.ws = max_norm, step.ws
+        if max_norm is not None:
+            _check_disjoint([(t.data_ptr(), 4 * t.numel()) for d in step.layers for t in (d["L"], d["dL"])])
+            nbytes = ctypes.c_size_t(0)
+            check(lib().lcp_clip_workspace_size(step.n, ctypes.byref(nbytes)))
+            self.grad_norm = torch.empty(1, dtype=torch.float32, device=step.ws.device)
+            if step.ws.numel() < nbytes.value:
+                self.ws = torch.empty(int(nbytes.value), dtype=torch.uint8, device=step.ws.device)
 
     def run(self, first: int, count: int, stream: Optional[torch.cuda.Stream] = None) -> None:
         s = self.step
+        if self.max_norm is not None:
+            check(lib().lcp_train_clip(s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count,
+                                       self.total, self.tau_start, self.tau_end, float(self.max_norm),
+                                       self.grad_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                                       _stream(stream)))
+            return
         check(lib().lcp_train(s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count,
                               self.total, self.tau_start, self.tau_end, s.ws.data_ptr(), s.ws.numel(),
                               _stream(stream)))
@@ -365,6 +517,123 @@ def sparse24_mm(vals: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, perm: O
                                 _ptr(perm, torch.int32, "perm"), _ptr(Y, torch.float32, "Y"), cout, cin, T, block,
                                 _dt(X), _stream(None)))
     return Y
+
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+GROUP8 = 128   # channels (and weight rows) that share a scale
+
+
+def _same_device(*tensors: Optional[torch.Tensor]) -> torch.device:
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("every tensor must be on one CUDA device")
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    return dev
+
+
+def _perm8(perm: Optional[torch.Tensor], cin: int) -> int:
+    """Block size of a permutation [C_in/B, B] (0 without one)."""
+    if perm is None:
+        return 0
+    if perm.dim() != 2 or perm.numel() != cin:
+        raise ValueError(f"perm must be [C_in/B, B] with {cin} entries, got {tuple(perm.shape)}")
+    return perm.shape[1]
+
+
+def _shaped(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def quant8(X: torch.Tensor, perm: Optional[torch.Tensor] = None, Q: Optional[torch.Tensor] = None,
+           S: Optional[torch.Tensor] = None):
+    """8-bit activations of X [T, C_in]: values (e4m3 [T, C_in]) and scales (e8m0 [T, ceil(C_in/128)]) of
+    x_pi = P_B^T x for the hard permutation perm [C_in/B, B], or of x itself."""
+    T, cin = X.shape
+    B = _perm8(perm, cin)
+    dev = _same_device(X, perm, Q, S)
+    Q = _shaped(Q, (T, cin), E4M3, dev, "Q")
+    S = _shaped(S, (T, (cin + GROUP8 - 1) // GROUP8), E8M0, dev, "S")
+    with _on_device(dev):
+        check(lib().lcp_quant8(_ptr(X, None, "X"), _ptr(perm, torch.int32, "perm"), _ptr(Q, E4M3, "Q"),
+                               _ptr(S, E8M0, "S"), T, cin, B, _dt(X), _stream(None)))
+    return Q, S
+
+
+def quant8_weight(W: torch.Tensor, perm: Optional[torch.Tensor] = None, mask_bits: Optional[torch.Tensor] = None,
+                  Q: Optional[torch.Tensor] = None, S: Optional[torch.Tensor] = None):
+    """8-bit weight: values (e4m3 [C_out, C_in]) and scales (e8m0 [ceil(C_out/128), ceil(C_in/128)]) of
+    A = M.(W P_B) for the hard permutation perm [C_in/B, B] and the packed mask bits of any N:M pattern
+    (either None: identity, nothing pruned)."""
+    cout, cin = W.shape
+    B = _perm8(perm, cin)
+    dev = _same_device(W, perm, mask_bits, Q, S)
+    if mask_bits is not None and mask_bits.numel() * 32 != cout * cin:
+        raise ValueError("mask_bits must be [C_out, C_in/32]")
+    Q = _shaped(Q, (cout, cin), E4M3, dev, "Q")
+    S = _shaped(S, ((cout + GROUP8 - 1) // GROUP8, (cin + GROUP8 - 1) // GROUP8), E8M0, dev, "S")
+    with _on_device(dev):
+        check(lib().lcp_quant8_weight(_ptr(W, None, "W"), _ptr(perm, torch.int32, "perm"),
+                                      _ptr(mask_bits, torch.int32, "mask"), _ptr(Q, E4M3, "Q"), _ptr(S, E8M0, "S"),
+                                      cout, cin, B, _dt(W), _stream(None)))
+    return Q, S
+
+
+def _check_weight8(Wq: torch.Tensor, Ws: torch.Tensor, cin: int) -> int:
+    cout = Wq.shape[0]
+    if Wq.dim() != 2 or Wq.shape[1] != cin:
+        raise ValueError(f"Wq must be [C_out, {cin}], got {tuple(Wq.shape)}")
+    if tuple(Ws.shape) != ((cout + GROUP8 - 1) // GROUP8, (cin + GROUP8 - 1) // GROUP8):
+        raise ValueError(f"Ws must be [ceil(C_out/128), ceil(C_in/128)], got {tuple(Ws.shape)}")
+    return cout
+
+
+def mm8(Xq: torch.Tensor, Xs: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, Y: Optional[torch.Tensor] = None,
+        out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """Y [T, C_out] = X W^T of two 8-bit operands with their scales (quant8, quant8_weight), in
+    float32 or bf16 (Y's dtype when Y is given)."""
+    T, cin = Xq.shape
+    cout = _check_weight8(Wq, Ws, cin)
+    if tuple(Xs.shape) != (T, (cin + GROUP8 - 1) // GROUP8):
+        raise ValueError(f"Xs must be [T, ceil(C_in/128)], got {tuple(Xs.shape)}")
+    dev = _same_device(Xq, Xs, Wq, Ws, Y)
+    Y = _shaped(Y, (T, cout), out_dtype, dev, "Y")
+    with _on_device(dev):
+        check(lib().lcp_mm8(_ptr(Xq, E4M3, "Xq"), _ptr(Xs, E8M0, "Xs"), _ptr(Wq, E4M3, "Wq"), _ptr(Ws, E8M0, "Ws"),
+                            _ptr(Y, None, "Y"), cout, cin, T, _dt(Y), _stream(None)))
+    return Y
+
+
+def linear8(Wq: torch.Tensor, Ws: torch.Tensor, X: torch.Tensor, perm: Optional[torch.Tensor] = None,
+            Y: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float32,
+            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The deployed 8-bit layer on activations X [T, C_in] (float32 or bf16): quant8 with the layer's
+    permutation, then mm8.  ``workspace``: uint8, at least linear8_workspace(T, C_in) bytes (allocated
+    here when None)."""
+    T, cin = X.shape
+    B = _perm8(perm, cin)
+    cout = _check_weight8(Wq, Ws, cin)
+    dev = _same_device(X, Wq, Ws, perm, Y, workspace)
+    Y = _shaped(Y, (T, cout), out_dtype, dev, "Y")
+    if workspace is None:
+        workspace = torch.empty(linear8_workspace(T, cin), dtype=torch.uint8, device=dev)
+    with _on_device(dev):
+        check(lib().lcp_linear8(_ptr(Wq, E4M3, "Wq"), _ptr(Ws, E8M0, "Ws"), _ptr(X, None, "X"),
+                                _ptr(perm, torch.int32, "perm"), _ptr(Y, None, "Y"), cout, cin, T, B, _dt(X), _dt(Y),
+                                _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(None)))
+    return Y
+
+
+def linear8_workspace(tokens: int, cin: int) -> int:
+    """Bytes of workspace linear8 needs."""
+    n = ctypes.c_size_t(0)
+    check(lib().lcp_linear8_workspace_size(tokens, cin, ctypes.byref(n)))
+    return int(n.value)
 
 
 def calib_gemm(X: torch.Tensor, W: torch.Tensor, At: Optional[torch.Tensor], Yd: torch.Tensor,

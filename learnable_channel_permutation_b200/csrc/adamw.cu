@@ -15,18 +15,6 @@
 namespace lcp {
 namespace {
 
-struct AdamCoef {
-  float b1, b2, c1, c2, eps, decay;   // c = 1 - b (formed in double), decay = 1 - lr wd
-  float step;                 // lr / (1 - b1^t)
-  float inv_sqrt_bc2;         // 1 / sqrt(1 - b2^t)
-};
-
-__device__ __forceinline__ void adam1(float& L, float g, float& m, float& v, const AdamCoef& c) {
-  m = c.b1 * m + c.c1 * g;
-  v = c.b2 * v + c.c2 * g * g;
-  L = L * c.decay - c.step * m / (sqrtf(v) * c.inv_sqrt_bc2 + c.eps);
-}
-
 __global__ void __launch_bounds__(256)
 adamw_kernel(float* __restrict__ L, const float* __restrict__ dL, float* __restrict__ m, float* __restrict__ v,
              long long quads, AdamCoef c) {
@@ -50,9 +38,7 @@ adamw_kernel(float* __restrict__ L, const float* __restrict__ dL, float* __restr
 
 }  // namespace
 
-lcp_status launch_adamw(float* L, const float* dL, float* m, float* v, long long n, double lr, double beta1,
-                        double beta2, double eps, double weight_decay, int t, cudaStream_t st) {
-  if (n == 0) return LCP_OK;
+AdamCoef adam_coef(double lr, double beta1, double beta2, double eps, double weight_decay, int t) {
   // every coefficient in double, rounded once
   const double bc1 = 1.0 - std::pow(beta1, (double)t);
   const double bc2 = 1.0 - std::pow(beta2, (double)t);
@@ -65,6 +51,13 @@ lcp_status launch_adamw(float* L, const float* dL, float* m, float* v, long long
   c.decay = (float)(1.0 - lr * weight_decay);
   c.step = (float)(lr / bc1);
   c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
+  return c;
+}
+
+lcp_status launch_adamw(float* L, const float* dL, float* m, float* v, long long n, double lr, double beta1,
+                        double beta2, double eps, double weight_decay, int t, cudaStream_t st) {
+  if (n == 0) return LCP_OK;
+  const AdamCoef c = adam_coef(lr, beta1, beta2, eps, weight_decay, t);
   const long long quads = n / 4;
   int sms = 148, dev = 0;
   cudaGetDevice(&dev);

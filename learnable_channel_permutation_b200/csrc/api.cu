@@ -12,6 +12,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -86,6 +87,7 @@ namespace {
   } while (0)
 
 constexpr int kMaxDim = 1 << 24;
+constexpr long long kMaxValues = 1LL << 40;   // values of a tensor list
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -595,14 +597,19 @@ lcp_status lcp_step_shard(const lcp_layer* layers, int nlayers, const lcp_hparam
   return step_impl(layers, nlayers, hp, ws, ws_bytes, stream, nullptr, 0, total_tokens, dP, ckpt);
 }
 
+static lcp_status check_adamw(const lcp_adamw_params* opt) {
+  if (!(opt->lr >= 0.0) || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) || !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) ||
+      !(opt->eps > 0.0) || !(opt->weight_decay >= 0.0) || !std::isfinite(opt->lr))
+    return fail(LCP_ERR_ARG, "AdamW parameters out of range");
+  return LCP_OK;
+}
+
 lcp_status lcp_adamw(float* L, const float* dL, float* m, float* v, long long n, const lcp_adamw_params* opt,
                      int t, cudaStream_t stream) {
   if (!L || !dL || !m || !v || !opt) return fail(LCP_ERR_NULL, "L, dL, m, v and opt are required");
   if (n < 0 || n % 4) return fail(LCP_ERR_SHAPE, "n = %lld must be a non-negative multiple of 4", n);
   if (t < 1) return fail(LCP_ERR_ARG, "t = %d must be >= 1", t);
-  if (!(opt->lr >= 0.0) || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) || !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) ||
-      !(opt->eps > 0.0) || !(opt->weight_decay >= 0.0) || !std::isfinite(opt->lr))
-    return fail(LCP_ERR_ARG, "AdamW parameters out of range");
+  LCP_TRY(check_adamw(opt));
   if (!aligned16(L) || !aligned16(dL) || !aligned16(m) || !aligned16(v))
     return fail(LCP_ERR_ARG, "every pointer must be 16-byte aligned");
   if (n == 0) return LCP_OK;
@@ -611,14 +618,14 @@ lcp_status lcp_adamw(float* L, const float* dL, float* m, float* v, long long n,
   return launch_adamw(L, dL, m, v, n, opt->lr, opt->beta1, opt->beta2, opt->eps, opt->weight_decay, t, stream);
 }
 
-lcp_status lcp_train(const lcp_layer* layers, int nlayers, const lcp_hparams* hp, const lcp_adamw_params* opt,
-                     const lcp_adamw_state* state, int first, int count, int total, float tau_start, float tau_end,
-                     void* ws, size_t ws_bytes, cudaStream_t stream) {
+// max_norm < 0: no clipping, an lcp_adamw a layer
+static lcp_status train_impl(const lcp_layer* layers, int nlayers, const lcp_hparams* hp, const lcp_adamw_params* opt,
+                             const lcp_adamw_state* state, int first, int count, int total, float tau_start,
+                             float tau_end, double max_norm, float* norm, void* ws, size_t ws_bytes,
+                             cudaStream_t stream) {
   if (!hp || !opt) return fail(LCP_ERR_NULL, "hp and opt are required");
   if (nlayers > 0 && !state) return fail(LCP_ERR_NULL, "state is required");
-  if (!(opt->lr >= 0.0) || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) || !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) ||
-      !(opt->eps > 0.0) || !(opt->weight_decay >= 0.0) || !std::isfinite(opt->lr))
-    return fail(LCP_ERR_ARG, "AdamW parameters out of range");
+  LCP_TRY(check_adamw(opt));
   if (total < 1 || first < 0 || count < 0 || first + count > total)
     return fail(LCP_ERR_ARG, "steps [%d, %d) outside a run of %d", first, first + count, total);
   if (!(tau_start > 0.f) || !(tau_end > 0.f) || !std::isfinite(tau_start) || !std::isfinite(tau_end))
@@ -628,18 +635,118 @@ lcp_status lcp_train(const lcp_layer* layers, int nlayers, const lcp_hparams* hp
     if (!aligned16(state[i].m) || !aligned16(state[i].v))
       return fail(LCP_ERR_ARG, "layer %d: AdamW moments must be 16-byte aligned", i);
   }
+  const bool clip = max_norm >= 0.0;
+  std::vector<lcp_adamw_tensor> list;
+  if (clip && nlayers > 0) {
+    if (!layers) return fail(LCP_ERR_NULL, "layers is NULL");
+    list.resize(nlayers);
+    for (int i = 0; i < nlayers; ++i)
+      list[i] = lcp_adamw_tensor{const_cast<float*>(layers[i].L), layers[i].dL, state[i].m, state[i].v,
+                                 (long long)layers[i].cin * hp->block};
+  }
   lcp_hparams h = *hp;
   for (int s = first; s < first + count; ++s) {
     const double frac = total > 1 ? (double)s / (double)(total - 1) : 0.0;
     h.tau = (float)((double)tau_start + ((double)tau_end - (double)tau_start) * frac);
     LCP_TRY(step_impl(layers, nlayers, &h, ws, ws_bytes, stream, nullptr, 0));
-    for (int i = 0; i < nlayers; ++i) {
+    // the partial sums of the norm lie in the step's workspace: the step's kernels are done with it by then
+    if (clip && nlayers > 0)
+      LCP_TRY(launch_adamw_list(list.data(), nlayers, *opt, s + 1, max_norm, norm, ws, stream));
+    for (int i = 0; i < nlayers && !clip; ++i) {
       const long long n = (long long)layers[i].cin * h.block;
       LCP_TRY(launch_adamw(const_cast<float*>(layers[i].L), layers[i].dL, state[i].m, state[i].v, n, opt->lr,
                            opt->beta1, opt->beta2, opt->eps, opt->weight_decay, s + 1, stream));
     }
   }
   return LCP_OK;
+}
+
+lcp_status lcp_train(const lcp_layer* layers, int nlayers, const lcp_hparams* hp, const lcp_adamw_params* opt,
+                     const lcp_adamw_state* state, int first, int count, int total, float tau_start, float tau_end,
+                     void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return train_impl(layers, nlayers, hp, opt, state, first, count, total, tau_start, tau_end, -1.0, nullptr, ws,
+                    ws_bytes, stream);
+}
+
+static lcp_status check_clip(int count, double max_norm, const float* norm, const void* ws, size_t ws_bytes) {
+  if (!norm) return fail(LCP_ERR_NULL, "norm is required");
+  if (((uintptr_t)norm & 3u) != 0) return fail(LCP_ERR_ARG, "norm must be 4-byte aligned");
+  if (count < 0 || count > kMaxDim) return fail(LCP_ERR_SHAPE, "count = %d", count);
+  if (!(max_norm > 0.0)) return fail(LCP_ERR_ARG, "max_norm must be positive");
+  if (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < clip_workspace(count))
+    return fail(LCP_ERR_WORKSPACE, "the workspace needs %zu bytes, 256-byte aligned", clip_workspace(count));
+  return LCP_OK;
+}
+
+lcp_status lcp_train_clip(const lcp_layer* layers, int nlayers, const lcp_hparams* hp, const lcp_adamw_params* opt,
+                          const lcp_adamw_state* state, int first, int count, int total, float tau_start,
+                          float tau_end, double max_norm, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  LCP_TRY(check_clip(nlayers, max_norm, norm, ws, ws_bytes));
+  return train_impl(layers, nlayers, hp, opt, state, first, count, total, tau_start, tau_end, max_norm, norm, ws,
+                    ws_bytes, stream);
+}
+
+lcp_status lcp_clip_workspace_size(int count, size_t* bytes) {
+  if (!bytes) return fail(LCP_ERR_NULL, "bytes is NULL");
+  if (count < 0 || count > kMaxDim) return fail(LCP_ERR_SHAPE, "count = %d", count);
+  *bytes = clip_workspace(count);
+  return LCP_OK;
+}
+
+static lcp_status check_grads(const lcp_grad* g, int count, bool out) {
+  if (count > 0 && !g) return fail(LCP_ERR_NULL, "the list is NULL");
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (g[i].dtype != LCP_F32 && g[i].dtype != LCP_BF16)
+      return fail(LCP_ERR_DTYPE, "tensor %d: unknown dtype %d", i, (int)g[i].dtype);
+    if (g[i].n < 0 || g[i].n > kMaxValues || (total += g[i].n) > kMaxValues)
+      return fail(LCP_ERR_SHAPE, "tensor %d: n = %lld (2^40 values in all at most)", i, g[i].n);
+    if (g[i].n == 0) continue;
+    if (!g[i].g || (out && !g[i].out)) return fail(LCP_ERR_NULL, "tensor %d: %s is NULL", i, g[i].g ? "out" : "g");
+    const uintptr_t e = g[i].dtype == LCP_F32 ? 3u : 1u;
+    if (((uintptr_t)g[i].g & e) || (out && ((uintptr_t)g[i].out & e)))
+      return fail(LCP_ERR_ARG, "tensor %d: not aligned to its element type", i);
+  }
+  return LCP_OK;
+}
+
+lcp_status lcp_grad_norm(const lcp_grad* grads, int count, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  LCP_TRY(check_clip(count, 1.0, norm, ws, ws_bytes));
+  LCP_TRY(check_grads(grads, count, false));
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  return launch_grad_norm(grads, count, norm, ws, stream);
+}
+
+lcp_status lcp_grad_clip(const lcp_grad* grads, int count, double max_norm, float* norm, void* ws, size_t ws_bytes,
+                         cudaStream_t stream) {
+  LCP_TRY(check_clip(count, max_norm, norm, ws, ws_bytes));
+  LCP_TRY(check_grads(grads, count, true));
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  return launch_grad_clip(grads, count, max_norm, norm, ws, stream);
+}
+
+lcp_status lcp_adamw_list(const lcp_adamw_tensor* tensors, int count, const lcp_adamw_params* opt, int t,
+                          double max_norm, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!opt) return fail(LCP_ERR_NULL, "opt is required");
+  LCP_TRY(check_clip(count, max_norm, norm, ws, ws_bytes));
+  LCP_TRY(check_adamw(opt));
+  if (t < 1) return fail(LCP_ERR_ARG, "t = %d must be >= 1", t);
+  if (count > 0 && !tensors) return fail(LCP_ERR_NULL, "the list is NULL");
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    const lcp_adamw_tensor& d = tensors[i];
+    if (d.n < 0 || d.n > kMaxValues || (total += d.n) > kMaxValues)
+      return fail(LCP_ERR_SHAPE, "tensor %d: n = %lld (2^40 values in all at most)", i, d.n);
+    if (d.n == 0) continue;
+    if (!d.L || !d.dL || !d.m || !d.v) return fail(LCP_ERR_NULL, "tensor %d: L, dL, m and v are required", i);
+    if (((uintptr_t)d.L | (uintptr_t)d.dL | (uintptr_t)d.m | (uintptr_t)d.v) & 3u)
+      return fail(LCP_ERR_ARG, "tensor %d: not aligned to its element type", i);
+  }
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  return launch_adamw_list(tensors, count, *opt, t, max_norm, norm, ws, stream);
 }
 
 lcp_status lcp_sinkhorn_fwd(const float* L, float* P, float* ckpt, int nblocks, int B, float tau,
@@ -769,6 +876,78 @@ lcp_status lcp_sparse24_mm(const void* values, const uint32_t* meta, const void*
   return launch_sparse24_mm(values, meta, X, perm, Y, cout, cin, tokens, B, dtype, stream);
 }
 
+// shapes and alignment shared by the 8-bit entry points (B is used with perm alone)
+static lcp_status check_8bit(int cout, int cin, const int32_t* perm, int B, int tokens, std::initializer_list<const void*> ptrs) {
+  LCP_TRY(check_infer_shape(cout, cin, B, perm != nullptr));
+  if (tokens < 0 || tokens > kMaxDim) return fail(LCP_ERR_SHAPE, "T = %d", tokens);
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(LCP_ERR_ARG, "pointers must be 16-byte aligned");
+  return LCP_OK;
+}
+
+lcp_status lcp_quant8(const void* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B,
+                      lcp_dtype dtype, cudaStream_t stream) {
+  if (tokens != 0 && (!X || !Q || !S)) return fail(LCP_ERR_NULL, "X, Q and S are required");
+  if (dtype != LCP_F32 && dtype != LCP_BF16) return fail(LCP_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+  LCP_TRY(check_8bit(1, cin, perm, B, tokens, {X, perm, Q, S}));
+  if (tokens == 0) return LCP_OK;
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  return launch_quant8(X, perm, Q, S, tokens, cin, B, dtype, stream);
+}
+
+lcp_status lcp_quant8_weight(const void* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S, int cout,
+                             int cin, int B, lcp_dtype dtype, cudaStream_t stream) {
+  if (!W || !Q || !S) return fail(LCP_ERR_NULL, "W, Q and S are required");
+  if (dtype != LCP_F32 && dtype != LCP_BF16) return fail(LCP_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+  LCP_TRY(check_8bit(cout, cin, perm, B, 1, {W, perm, mask, Q, S}));
+  if (cout > 128 * 65535) return fail(LCP_ERR_SHAPE, "C_out = %d is above %d", cout, 128 * 65535);
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  return launch_quant8_weight(W, perm, mask, Q, S, cout, cin, B, dtype, stream);
+}
+
+lcp_status lcp_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, void* Y, int cout,
+                   int cin, int tokens, lcp_dtype ydtype, cudaStream_t stream) {
+  if (!Wq || !Ws || (tokens != 0 && (!Xq || !Xs || !Y)))
+    return fail(LCP_ERR_NULL, "Xq, Xs, Wq, Ws and Y are required");
+  if (ydtype != LCP_F32 && ydtype != LCP_BF16) return fail(LCP_ERR_DTYPE, "unknown output dtype %d", (int)ydtype);
+  LCP_TRY(check_8bit(cout, cin, nullptr, 0, tokens, {Xq, Xs, Wq, Ws, Y}));
+  if (tokens == 0) return LCP_OK;
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  return launch_mm8(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, ydtype, false, stream);
+}
+
+static size_t linear8_scales_at(int tokens, int cin) { return ((size_t)tokens * cin + 255) & ~(size_t)255; }
+
+lcp_status lcp_linear8_workspace_size(int tokens, int cin, size_t* bytes) {
+  if (!bytes) return fail(LCP_ERR_NULL, "bytes is NULL");
+  LCP_TRY(check_8bit(1, cin, nullptr, 0, tokens, {}));
+  *bytes = linear8_scales_at(tokens, cin) + (size_t)tokens * ((cin + 127) / 128);
+  return LCP_OK;
+}
+
+lcp_status lcp_linear8(const uint8_t* Wq, const uint8_t* Ws, const void* X, const int32_t* perm, void* Y, int cout,
+                       int cin, int tokens, int B, lcp_dtype dtype, lcp_dtype ydtype, void* ws, size_t ws_bytes,
+                       cudaStream_t stream) {
+  if (!Wq || !Ws || (tokens != 0 && (!X || !Y))) return fail(LCP_ERR_NULL, "Wq, Ws, X and Y are required");
+  if (dtype != LCP_F32 && dtype != LCP_BF16) return fail(LCP_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+  if (ydtype != LCP_F32 && ydtype != LCP_BF16) return fail(LCP_ERR_DTYPE, "unknown output dtype %d", (int)ydtype);
+  LCP_TRY(check_8bit(cout, cin, perm, B, tokens, {Wq, Ws, X, perm, Y}));
+  if (tokens == 0) return LCP_OK;
+  size_t need = 0;
+  LCP_TRY(lcp_linear8_workspace_size(tokens, cin, &need));
+  if (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < need)
+    return fail(LCP_ERR_WORKSPACE, "the workspace needs %zu bytes, 256-byte aligned", need);
+  LCP_TRY(check_arch());
+  LCP_TRY(check_pending());
+  uint8_t* q = static_cast<uint8_t*>(ws);
+  uint8_t* s = q + linear8_scales_at(tokens, cin);
+  LCP_TRY(launch_quant8(X, perm, q, s, tokens, cin, B, dtype, stream));
+  return launch_mm8(q, s, Wq, Ws, Y, cout, cin, tokens, ydtype, true, stream);
+}
+
 lcp_status nm_mask(const void* Wp, uint32_t* mask_bits, int rows, int cols, int n, int m,
                    lcp_dtype dtype, cudaStream_t stream) {
   if (!Wp || !mask_bits) return fail(LCP_ERR_NULL, "Wp and mask_bits are required");
@@ -876,7 +1055,7 @@ extern "C" lcp_status lcp_device_error(int* site, int reset) {
   using namespace lcp;
   if (!site) return fail(LCP_ERR_NULL, "site is NULL");
   lcp_status (*const readers[])(int*, int) = {tc_error_gemm, tc_error_permute, tc_error_block_bwd, harden_error,
-                                               infer_error, tc_error_infer};
+                                               infer_error, tc_error_infer, quant_error, tc_error_mm8};
   int first = 0;
   for (auto rd : readers) {
     int v = 0;

@@ -257,6 +257,29 @@ lcp_status harden_error(int* site, int reset);
 lcp_status launch_score(const void* W, const void* X, void* S, float* stats, int cout, int cin, int tokens, int kind,
                         lcp_dtype dt, cudaStream_t st);
 
+// AdamW of one value (adamw.cu): c holds every coefficient, formed in double and
+// rounded once.
+struct AdamCoef {
+  float b1, b2, c1, c2, eps, decay;   // c = 1 - b, decay = 1 - lr wd
+  float step;                 // lr / (1 - b1^t)
+  float inv_sqrt_bc2;         // 1 / sqrt(1 - b2^t)
+};
+AdamCoef adam_coef(double lr, double beta1, double beta2, double eps, double weight_decay, int t);
+__device__ __forceinline__ void adam1(float& L, float g, float& m, float& v, const AdamCoef& c) {
+  m = c.b1 * m + c.c1 * g;
+  v = c.b2 * v + c.c2 * g * g;
+  L = L * c.decay - c.step * m / (sqrtf(v) * c.inv_sqrt_bc2 + c.eps);
+}
+
+// The gradient norm over a list of tensors, clipping by it, and one AdamW update of a
+// list with the clipping factor (clip.cu).  ws: clip_workspace(count) bytes.
+constexpr int kClipCtasPerSm = 8;
+size_t clip_workspace(int count);
+lcp_status launch_grad_norm(const lcp_grad* d, int count, float* norm, void* ws, cudaStream_t st);
+lcp_status launch_grad_clip(const lcp_grad* d, int count, double max_norm, float* norm, void* ws, cudaStream_t st);
+lcp_status launch_adamw_list(const lcp_adamw_tensor* d, int count, const lcp_adamw_params& opt, int step, double max_norm,
+                             float* norm, void* ws, cudaStream_t st);
+
 // AdamW over n float32 values (n a multiple of 4), t the 1-based step.
 lcp_status launch_adamw(float* L, const float* dL, float* m, float* v, long long n, double lr, double beta1,
                         double beta2, double eps, double weight_decay, int t, cudaStream_t st);
@@ -278,6 +301,18 @@ lcp_status launch_sparse24_tc(const __nv_bfloat16* vals, const uint32_t* meta, c
                               cudaStream_t st);
 lcp_status tc_error_infer(int* site, int reset);
 lcp_status infer_error(int* site, int reset);
+
+// 8-bit operands (e4m3 values, e8m0 scales of 128-blocks) and their product.
+// w_early: the kernel before on the stream does not write Wq or Ws, so the weight
+// may be read before that kernel has finished.
+lcp_status launch_quant8(const void* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B,
+                         lcp_dtype dt, cudaStream_t st);
+lcp_status launch_quant8_weight(const void* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S,
+                                int cout, int cin, int B, lcp_dtype dt, cudaStream_t st);
+lcp_status launch_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, void* Y, int cout,
+                      int cin, int tokens, lcp_dtype ydt, bool w_early, cudaStream_t st);
+lcp_status quant_error(int* site, int reset);
+lcp_status tc_error_mm8(int* site, int reset);
 
 // Device error words of the tensor-core translation units: the first wait
 // site that timed out since the last reset, 0 if none (cleared when `reset`).

@@ -1,0 +1,284 @@
+// 8-bit operands of the deployed product: e4m3 values with one power-of-two
+// scale (e8m0) for each block of 128.
+//
+//   activations: a block is 128 consecutive channels of one token of x_pi
+//   weights:     a block is 128 rows x 128 columns of A = M.(W P_B)
+//
+// The scale of a block with largest magnitude amax is 2^k, k the smallest
+// integer >= -127 with amax <= 448 2^k (448 is e4m3's largest value; k = 0 for a
+// block of zeros), and a value becomes q = rn_e4m3(x 2^-k).  The product x 2^-k
+// only moves the exponent, so the rounding to e4m3 (to nearest, ties to even;
+// at most half a step, 2^-4 of the value) is the only one made.  A block that
+// holds an infinity or a NaN gets the NaN scale (0xff) and NaN values, so every
+// product it enters is NaN.
+//
+// Both kernels are bound by HBM: they read each value once and write half (bf16)
+// or a quarter (float32) of the bytes.  The permutation is applied by a warp on
+// its own 256 channels (whole blocks for every B <= 256), through 256 values of
+// shared memory that only that warp uses: no CTA barrier.
+
+#include <cuda_fp8.h>
+
+#include "lcp_internal.cuh"
+
+namespace lcp {
+namespace {
+
+__device__ int g_quant_error;   // first invalid permutation entry seen (302), 0 if none
+
+constexpr int Q8_CHUNK = 256;      // channels of a warp: two scale groups, eight channels a lane
+constexpr int Q8_ROW_WARPS = 8;    // activations: warps per CTA
+constexpr int Q8_W_WARPS = 16;     // weights: warps per CTA
+constexpr int Q8_W_ROWS = 128 / Q8_W_WARPS;   // weight rows of a warp
+
+// |x| of float bits, comparable as an integer: infinities above every finite
+// value and NaNs above those.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// e8m0 byte of a block's largest magnitude.  amax = 1.f 2^(e - 127) is at most
+// 448 2^k = 1.75 2^(k + 8) for k = e - 135 when f <= .75, else for k = e - 134.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  if (amax >= 0x7f800000u) return 255u;
+  if (amax == 0u) return 127u;
+  const int byte = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return byte < 0 ? 0u : (uint32_t)byte;
+}
+// 2^(127 - byte): a normal float for every byte scale_byte returns for finite
+// blocks (0 .. 247); NaN for the NaN scale
+__device__ __forceinline__ float scale_inverse(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - byte) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack4_e4m3(const float* v, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Eight consecutive values of a row, 16-byte loads.
+template <typename T> struct Vec8 { uint4 u[sizeof(T) / 2]; };
+template <typename T> __device__ __forceinline__ Vec8<T> load8(const T* p) {
+  Vec8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+template <typename T> __device__ __forceinline__ Vec8<T> zero8() {
+  Vec8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = make_uint4(0u, 0u, 0u, 0u);
+  return r;
+}
+
+// The slots (0 .. 255) of a lane's eight source channels in the warp's chunk;
+// -1 for a permutation entry outside [0, B).
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int cin, int bmask, int (&slot)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int p = chan + j < cin ? __ldg(perm + chan + j) : ((chan + j) & bmask);
+    if (p < 0 || p > bmask) {
+      atomicCAS(&g_quant_error, 0, 302);
+      slot[j] = -1;
+    } else {
+      slot[j] = ((chan + j) & (Q8_CHUNK - 1) & ~bmask) | p;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> permute8(const Vec8<T>& v, const int (&slot)[8], T* buf, int lane) {
+  const T* e = reinterpret_cast<const T*>(&v);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (slot[j] >= 0) buf[slot[j]] = e[j];
+  __syncwarp();
+  Vec8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(buf + 8 * lane)[i];
+  return r;
+}
+
+template <typename T> __device__ __forceinline__ void to_f32x8(const Vec8<T>& v, float (&f)[8]) {
+  const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = to_f32(e[j]);
+}
+__device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(f[j]));
+  return m;
+}
+// over the 16 lanes that share a scale group
+__device__ __forceinline__ uint32_t half_max(uint32_t m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// Activations.  A warp keeps one 256-channel chunk and walks tokens, two at a
+// time, so the permutation is read once and its slots stay in registers.
+template <typename T, bool PERM>
+__global__ void __launch_bounds__(32 * Q8_ROW_WARPS)
+quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, uint8_t* __restrict__ Q,
+                   uint8_t* __restrict__ S, int tokens, int cin, int bmask) {
+  constexpr int UN = 2;
+  __shared__ __align__(16) T stage[PERM ? Q8_ROW_WARPS : 1][PERM ? UN : 1][PERM ? Q8_CHUNK : 8];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
+  const int G = (cin + 127) / 128;
+  const bool in = chan < cin;      // C_in is a multiple of 32: a lane's channels are inside together
+  pdl_wait();
+  pdl_trigger();
+  int slot[8];
+  if (PERM) load_slots(perm, chan, cin, bmask, slot);
+  const int step = gridDim.y * Q8_ROW_WARPS;
+  for (int t0 = blockIdx.y * Q8_ROW_WARPS + warp; t0 < tokens; t0 += UN * step) {
+    Vec8<T> v[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int t = t0 + u * step;
+      v[u] = in && t < tokens ? load8(X + (size_t)t * cin + chan) : zero8<T>();
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int t = t0 + u * step;
+      if (t >= tokens) break;        // uniform over the warp
+      if (PERM) v[u] = permute8(v[u], slot, stage[warp][u], lane);
+      float f[8];
+      to_f32x8(v[u], f);
+      const uint32_t byte = scale_byte(half_max(amax8(f)));
+      const float inv = scale_inverse(byte);
+      if (in) {
+        *reinterpret_cast<uint2*>(Q + (size_t)t * cin + chan) = make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
+        if ((lane & 15) == 0) S[(size_t)t * G + chan / 128] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+// Weights.  A CTA takes 128 rows x 256 channels (two blocks), eight rows a warp,
+// and holds the values in registers (in their stored type) while the two block
+// maxima are reduced.
+template <typename T, bool PERM, bool MASK>
+__global__ void __launch_bounds__(32 * Q8_W_WARPS)
+quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, const uint8_t* __restrict__ mask,
+                     uint8_t* __restrict__ Q, uint8_t* __restrict__ S, int cout, int cin, int bmask) {
+  __shared__ __align__(16) T stage[PERM ? Q8_W_WARPS : 1][PERM ? Q8_CHUNK : 8];
+  __shared__ uint32_t part[Q8_W_WARPS][2];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
+  const int G = (cin + 127) / 128;
+  const bool in = chan < cin;
+  pdl_wait();
+  pdl_trigger();
+  int slot[8];
+  if (PERM) load_slots(perm, chan, cin, bmask, slot);
+  Vec8<T> v[Q8_W_ROWS];
+  uint32_t keep[Q8_W_ROWS];
+#pragma unroll
+  for (int r = 0; r < Q8_W_ROWS; ++r) {
+    const int o = blockIdx.y * 128 + r * Q8_W_WARPS + warp;
+    const bool ok = in && o < cout;
+    v[r] = ok ? load8(W + (size_t)o * cin + chan) : zero8<T>();
+    keep[r] = MASK && ok ? (uint32_t)__ldg(mask + (size_t)o * (cin / 8) + chan / 8) : 0xffu;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int r = 0; r < Q8_W_ROWS; ++r) {
+    if (PERM) v[r] = permute8(v[r], slot, stage[warp], lane);
+    if (MASK) {
+      T* e = reinterpret_cast<T*>(&v[r]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!((keep[r] >> j) & 1u)) e[j] = from_f32<T>(0.f);
+    }
+    float f[8];
+    to_f32x8(v[r], f);
+    m = max(m, amax8(f));
+  }
+  m = half_max(m);
+  if ((lane & 15) == 0) part[warp][lane >> 4] = m;
+  __syncthreads();
+  m = 0;
+#pragma unroll
+  for (int w = 0; w < Q8_W_WARPS; ++w) m = max(m, part[w][lane >> 4]);
+  const uint32_t byte = scale_byte(m);
+  const float inv = scale_inverse(byte);
+  if (!in) return;
+#pragma unroll
+  for (int r = 0; r < Q8_W_ROWS; ++r) {
+    const int o = blockIdx.y * 128 + r * Q8_W_WARPS + warp;
+    if (o >= cout) break;
+    float f[8];
+    to_f32x8(v[r], f);
+    *reinterpret_cast<uint2*>(Q + (size_t)o * cin + chan) = make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
+  }
+  if (warp == 0 && (lane & 15) == 0) S[(size_t)blockIdx.y * G + chan / 128] = (uint8_t)byte;
+}
+
+int cdiv_host(int a, int b) { return (a + b - 1) / b; }
+
+template <typename T>
+lcp_status rows_t(const T* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B, cudaStream_t st) {
+  int sms = 148, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int chunks = cdiv_host(cin, Q8_CHUNK);
+  // enough CTAs for two rounds of eight on every SM, each warp walking the rest of the tokens
+  int gy = cdiv_host(tokens, Q8_ROW_WARPS);
+  const int most = cdiv_host(16 * sms, chunks);
+  if (gy > most) gy = most;
+  if (gy > 65535) gy = 65535;
+  const dim3 grid((unsigned)chunks, (unsigned)gy);
+  const int bmask = perm ? B - 1 : 0;
+  if (perm)
+    return launch_kernel(quant8_rows_kernel<T, true>, grid, dim3(32 * Q8_ROW_WARPS), 0, st, 1, true, "quant8", X, perm, Q,
+                         S, tokens, cin, bmask);
+  return launch_kernel(quant8_rows_kernel<T, false>, grid, dim3(32 * Q8_ROW_WARPS), 0, st, 1, true, "quant8", X, perm, Q, S,
+                       tokens, cin, bmask);
+}
+
+template <typename T>
+lcp_status weight_t(const T* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S, int cout, int cin,
+                    int B, cudaStream_t st) {
+  const dim3 grid((unsigned)cdiv_host(cin, Q8_CHUNK), (unsigned)cdiv_host(cout, 128)), block(32 * Q8_W_WARPS);
+  const uint8_t* mb = reinterpret_cast<const uint8_t*>(mask);
+  const int bmask = perm ? B - 1 : 0;
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, grid, block, 0, st, 1, true, "quant8_weight", W, perm, mb, Q, S, cout, cin, bmask);
+  };
+  if (perm) return mask ? go(quant8_weight_kernel<T, true, true>) : go(quant8_weight_kernel<T, true, false>);
+  return mask ? go(quant8_weight_kernel<T, false, true>) : go(quant8_weight_kernel<T, false, false>);
+}
+
+}  // namespace
+
+lcp_status quant_error(int* site, int reset) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_quant_error, sizeof(int));
+  if (e == cudaSuccess && reset) {
+    const int z = 0;
+    e = cudaMemcpyToSymbol(g_quant_error, &z, sizeof(int));
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(LCP_ERR_CUDA, "reading the device error word: %s", cudaGetErrorString(e));
+  }
+  *site = v;
+  return LCP_OK;
+}
+
+lcp_status launch_quant8(const void* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B,
+                         lcp_dtype dt, cudaStream_t st) {
+  if (dt == LCP_F32) return rows_t(static_cast<const float*>(X), perm, Q, S, tokens, cin, B, st);
+  return rows_t(static_cast<const __nv_bfloat16*>(X), perm, Q, S, tokens, cin, B, st);
+}
+
+lcp_status launch_quant8_weight(const void* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S,
+                                int cout, int cin, int B, lcp_dtype dt, cudaStream_t st) {
+  if (dt == LCP_F32) return weight_t(static_cast<const float*>(W), perm, mask, Q, S, cout, cin, B, st);
+  return weight_t(static_cast<const __nv_bfloat16*>(W), perm, mask, Q, S, cout, cin, B, st);
+}
+
+}  // namespace lcp

@@ -502,3 +502,92 @@ def sparse24_mm(vals: np.ndarray, idx: np.ndarray, X_tokens: np.ndarray,
         Y[:, r0:r1] = np.einsum("ok,tok->to", vals[r0:r1], Xp[:, slot[r0:r1]])
     return Y
 
+
+
+# 8-bit storage: e4m3 values with one power-of-two scale for each block of 128
+# (activations: a token's 128 channels; weights: 128 rows x 128 columns).
+
+E4M3_MAX = 448.0
+
+
+def e4m3_round(x: np.ndarray) -> np.ndarray:
+    """Nearest e4m3 value (four exponent bits of bias 7, three fraction bits, no
+    infinities, largest 448) of |x| <= 448, ties to the even fraction."""
+    x = np.asarray(x, np.float64)
+    _, e = np.frexp(x)                                   # |x| in [2^(e-1), 2^e)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.round(x / step) * step
+
+
+def block_exponent(amax: float) -> int:
+    """The smallest k >= -127 with amax <= 448 2^k; 0 for a block of zeros."""
+    if amax == 0:
+        return 0
+    k = -127
+    while amax > E4M3_MAX * 2.0 ** k:
+        k += 1
+    return k
+
+
+def _quantise_block(v: np.ndarray) -> Tuple[np.ndarray, float]:
+    if not np.all(np.isfinite(v)):
+        return np.full(v.shape, np.nan), float("nan")
+    k = block_exponent(float(np.max(np.abs(v))) if v.size else 0.0)
+    return e4m3_round(v * 2.0 ** -k), 2.0 ** k
+
+
+def quant8(X_tokens: np.ndarray, perm: Optional[np.ndarray] = None) -> Tuple[np.ndarray, np.ndarray]:
+    """(values [T, C_in], scales [T, ceil(C_in / 128)]) of x_pi (``perm`` None: of x)."""
+    X = np.asarray(X_tokens, np.float64)
+    if perm is not None:
+        X = gather_channels(X, perm)
+    T, cin = X.shape
+    q, s = np.empty_like(X), np.empty((T, -(-cin // 128)))
+    for t in range(T):
+        for g in range(s.shape[1]):
+            q[t, 128 * g:128 * g + 128], s[t, g] = _quantise_block(X[t, 128 * g:128 * g + 128])
+    return q, s
+
+
+def quant8_weight(W: np.ndarray, perm: Optional[np.ndarray] = None,
+                  mask: Optional[np.ndarray] = None) -> Tuple[np.ndarray, np.ndarray]:
+    """(values [C_out, C_in], scales [ceil(C_out / 128), ceil(C_in / 128)]) of A = M.(W P_B)."""
+    A = np.asarray(W, np.float64)
+    if perm is not None:
+        A = gather_channels(A, perm)                     # W P_B moves columns as x_pi moves channels
+    if mask is not None:
+        A = np.where(mask, A, 0.0)
+    rows, cols = A.shape
+    q, s = np.empty_like(A), np.empty((-(-rows // 128), -(-cols // 128)))
+    for r in range(s.shape[0]):
+        for g in range(s.shape[1]):
+            at = np.s_[128 * r:128 * r + 128, 128 * g:128 * g + 128]
+            q[at], s[r, g] = _quantise_block(A[at])
+    return q, s
+
+
+def dequant8(q: np.ndarray, s: np.ndarray, rows_per_scale: int) -> np.ndarray:
+    """The values an 8-bit operand stands for."""
+    q = np.asarray(q, np.float64)
+    s = np.repeat(np.repeat(np.asarray(s, np.float64), rows_per_scale, axis=0), 128, axis=1)
+    return q * s[:q.shape[0], :q.shape[1]]
+
+
+def mm8(Xq, Xs, Wq, Ws) -> np.ndarray:
+    """Y[t, o] = sum_c x[t, c] w[o, c] of the values the operands stand for."""
+    return dequant8(Xq, Xs, 1) @ dequant8(Wq, Ws, 128).T
+
+
+# ---------------------------------------------------------------------------
+# Gradient norm over many tensors and clipping (the library's extension)
+# ---------------------------------------------------------------------------
+
+def grad_norm(grads) -> float:
+    """2-norm over every value of every tensor."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        return float(np.sqrt(sum(float(np.sum(np.square(np.asarray(g, np.float64)))) for g in grads)))
+
+
+def clip_factor(norm: float, max_norm: float) -> float:
+    f = max_norm / (norm + 1e-6) if np.isfinite(max_norm) else float("inf") if np.isfinite(norm) else float("nan")
+    return f if np.isnan(f) else min(1.0, f)
