@@ -26,6 +26,37 @@ __device__ __forceinline__ void mma_mx8(uint32_t d, uint64_t a, uint64_t b, uint
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
+// The same on a CTA pair: M = 256, each CTA's 128 rows of A, half of B's rows, A scales of its
+// own rows and B scales of all N rows.
+__device__ __forceinline__ void mma_mx8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// Each CTA of the pair copies from its own shared memory into its own tensor memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t sd) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sd) : "memory");
+}
+// Arrival on, and wait for, a barrier of the pair that announces plain shared-memory writes of
+// either CTA (cluster scope).
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // 32 rows of 16 bytes of shared memory to four columns of tensor memory, the same
 // in every 32-lane quarter: lane r's column j is word j of row r.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sd) {
@@ -44,16 +75,62 @@ __device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int byte) {
   return idesc | ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
 }
 
+// One thread of a converged warp.  The loops that issue TMA copies and products run on it: a
+// region the compiler knows to be one thread's issues a product in ~40 cycles, one under
+// `lane == 0` in ~75 (its operands move to uniform registers one by one), which would bound the
+// kernels (measured on four products and a commit: 157 cycles against 305).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Waits of those two threads.  Their loops have no exit on a wait that gave up: a break there makes
+// the loop's values per-thread ones again (338 cycles against 206 for a wait, four products and a
+// commit).  Instead, once a wait of the CTA has given up, each later one returns at once, and the
+// loops run out over operands that are no longer meant to be right.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site) {
+  if (!*abort_flag) mbar_wait_slow(bar, parity, abort_flag, site);
+}
+__device__ __forceinline__ void wait_through(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site) {
+  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort_flag, site);
+}
+// The same on a barrier that announces plain writes of both CTAs of a pair.
+__device__ __noinline__ void wait_slow_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site) {
+  if (!*abort_flag) mbar_wait_slow(bar, parity, abort_flag, site);
+  mbar_try_wait_cluster(bar, parity);     // the acquire of the completed phase
+}
+__device__ __forceinline__ void wait_through_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site) {
+  if (!mbar_try_wait_cluster(bar, parity)) wait_slow_cluster(bar, parity, abort_flag, site);
+}
+
 constexpr int M8_BM = 128;            // output channels of a CTA: one row of weight scales
 constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one scale group of channels)
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
 constexpr int M8_THREADS = 224;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6: scales
 constexpr int M8_MAX_STAGES = 8;
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
+}
+// Four consecutive outputs, `left` of them inside the row; whole rows of four are aligned.
+template <typename OUT> __device__ __forceinline__ void store4(OUT* out, const float4& s, int left, bool whole) {
+  if (whole) {
+    if (left <= 0) return;
+    if constexpr (sizeof(OUT) == 4) *reinterpret_cast<float4*>(out) = s;
+    else *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    return;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) out[i] = from_f32<OUT>(v[i]);
 }
 
 // One CTA: 128 output channels x NT tokens over a range of scale groups; the S CTAs of a
@@ -115,7 +192,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const uint32_t tmem = *holder;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t issued = 0, issued_par = 0;
       const int ahead = w_early ? min(stages, nk) : 0;
       for (int k = 0; k < ahead; ++k) {
@@ -127,7 +204,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       int stage = 0;
       uint32_t ph = 0;
       for (int k = 0; k < nk; ++k) {
-        if (!mbar_wait(empty(stage), ph ^ 1u, abort_flag, 401)) break;
+        wait_through(empty(stage), ph ^ 1u, abort_flag, 401);
         issued |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (ph << stage);
         const uint32_t dst = smem_u32(smem + stage * stage_bytes);
@@ -143,28 +220,32 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = idesc_mx8(M8_BM, NT);
+      const uint64_t wd0 = sdesc(smem_u32(smem), 16, 1024), xd0 = sdesc(smem_u32(smem) + M8_A, 16, 1024);
       int stage = 0;
       uint32_t ph = 0;
-      bool ok = true;
-      for (int c = 0; c < nchunk && ok; ++c) {
+      for (int c = 0; c < nchunk; ++c) {
         const int slot = c % M8_SF;
-        if (!mbar_wait(sffull(slot), (uint32_t)(c / M8_SF) & 1u, abort_flag, 403)) break;
-        if (c >= 2 && !mbar_wait(sfempty((c - 2) % M8_SF), (uint32_t)((c - 2) / M8_SF) & 1u, abort_flag, 404)) break;
+        wait_through(sffull(slot), (uint32_t)(c / M8_SF) & 1u, abort_flag, 403);
+        if (c >= 2) wait_through(sfempty((c - 2) % M8_SF), (uint32_t)((c - 2) / M8_SF) & 1u, abort_flag, 404);
         tc_fence_after();
         const uint32_t sfa = tmem + (uint32_t)(NT + 8 * (c & 1)), sfb = sfa + 4;
         copy_scales(sfa, sdesc_scales(smem_u32(sf + slot * 1024)));
         copy_scales(sfb, sdesc_scales(smem_u32(sf + slot * 1024 + 512)));
-        for (int j = 0; j < 4 && 4 * c + j < nk; ++j) {
-          if (!mbar_wait(full(stage), ph, abort_flag, 405)) { ok = false; break; }
+        const int jn = min(4, nk - 4 * c);
+        for (int j = 0; j < jn; ++j) {
+          wait_through(full(stage), ph, abort_flag, 405);
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * stage_bytes), b0 = a0 + M8_A;
+          const uint64_t wd = wd0 + (uint32_t)(stage * (stage_bytes >> 4)), xd = xd0 + (uint32_t)(stage * (stage_bytes >> 4));
           const int left = cin - (g0 + 4 * c + j) * 128;
-          const int steps = left >= 128 ? 4 : left / 32;     // C_in is a multiple of 32
           const uint32_t id = with_byte(idesc, j);
-          for (int k = 0; k < steps; ++k)
-            mma_mx8(tmem, sdesc(a0 + k * 32, 16, 1024), sdesc(b0 + k * 32, 16, 1024), id, sfa, sfb, (c | j | k) != 0);
+          if (left >= 128) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_mx8(tmem, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
+          } else {                                           // C_in is a multiple of 32
+            for (int k = 0; k < left / 32; ++k) mma_mx8(tmem, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
+          }
           mma_commit(empty(stage));
           if (++stage == stages) { stage = 0; ph ^= 1u; }
         }
@@ -227,18 +308,26 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   tc_fence_before();
   if (S > 1) {
     cluster_sync_all();     // every CTA's partial result is written
-    if (warp >= 2 && warp < 6) {
-      const int i = (warp - 2) * 32 + lane, o = mt * M8_BM + i;
-      const uint32_t mine = smem_u32(smem) + 4u * (uint32_t)i;
-      for (int n = rank; n < NT && t0 + n < tokens; n += S) {
-        float v[8];
+    // a warp adds a token's 128 channels, four a lane; the tokens of this rank go round the warps
+    const uint32_t mine = smem_u32(smem) + 16u * (uint32_t)lane;
+    const int o = mt * M8_BM + 4 * lane;
+    const int nmax = min(NT, tokens - t0);
+#pragma unroll 2
+    for (int n = rank + S * warp; n < nmax; n += S * (M8_THREADS / 32)) {
+      float4 v[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = r < S ? ld_cluster_f32(mapa(mine + (uint32_t)n * 512u, (uint32_t)r)) : 0.f;
-        float s = v[0];
+      for (int r = 0; r < 8; ++r)
+        if (r < S) v[r] = ld_cluster_f32x4(mapa(mine + (uint32_t)n * 512u, (uint32_t)r));
+      float4 s = v[0];
 #pragma unroll
-        for (int r = 1; r < 8; ++r) s += v[r];
-        if (o < cout) Y[(size_t)(t0 + n) * cout + o] = from_f32<OUT>(s);
-      }
+      for (int r = 1; r < 8; ++r)
+        if (r < S) {
+          s.x += v[r].x;
+          s.y += v[r].y;
+          s.z += v[r].z;
+          s.w += v[r].w;
+        }
+      store4(Y + (size_t)(t0 + n) * cout + o, s, cout - o, (cout & 3) == 0);
     }
     cluster_sync_all();     // no CTA leaves while another reads its partial result
   } else {
@@ -247,6 +336,264 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, ncols);
+  }
+}
+
+// Four scale bytes of a row staged in shared memory, groups g .. g + 3 (unit scale past the last
+// group).  The aligned words around them are read whole: up to seven bytes past the row, which
+// is still shared memory of the kernel.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int g, int G) {
+  const uint32_t a = smem_u32(row + g), b = a & ~3u;
+  uint32_t lo, hi;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(b));
+  if ((G & 3) == 0) return lo;                                   // rows 4-byte aligned, g a multiple of 4
+  asm volatile("ld.shared.u32 %0, [%1+4];" : "=r"(hi) : "r"(b));
+  const uint32_t w = __funnelshift_r(lo, hi, 8u * (a & 3u));
+  const int left = G - g;
+  return left >= 4 ? w : (w & ~(0xffffffffu << (8 * left))) | (0x7f7f7f7fu << (8 * left));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Many tokens: persistent CTA pairs (cta_group::2) on tiles of 256 output channels x N tokens.
+// Each CTA stages its 128 rows of W and its half of the tile's tokens, the leader issues
+// M = 256 products over both, and each CTA keeps its 128 channels x N tokens of the result in one
+// of two accumulators, so the next tile's products run while the epilogue stores this one.
+// Columns: two accumulators of N, then two sets of scales (4 of W, 8 of X): N <= 240.
+constexpr int P8_THREADS = 320;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6-9: scales (128 tokens, every other chunk)
+constexpr int P8_SF_BYTES = 1536;     // a chunk's scale words: 512 B of W, 2 x 512 B of X
+constexpr int P8_MAX_N = 240;
+constexpr int P8_MAX_G = 256;         // C_in <= 32768: a tile's scale bytes are staged whole
+constexpr int P8_RAW = 40 * 1024;     // their room at most: N G <= 40 KB
+constexpr int P8_MAX_STAGES = 10;
+
+template <typename OUT>
+__global__ void __launch_bounds__(P8_THREADS, 1)
+mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const uint8_t* __restrict__ Xs, const uint8_t* __restrict__ Ws, OUT* __restrict__ Y, int cout, int cin,
+                int tokens, int N, int stages, int raw_bytes, int tokens_fast) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const int stage_bytes = M8_A + N * 64;
+  uint8_t* sf = smem + stages * stage_bytes;
+  uint8_t* wraw = sf + M8_SF * P8_SF_BYTES;      // the tile's W scales (one row), then its X scales (N rows)
+  uint8_t* xraw = wraw + P8_MAX_G;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(xraw + raw_bytes);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * P8_MAX_STAGES + 2 * M8_SF + 6);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
+  auto full = [&](int s) { return smem_u32(bars + s); };                       // leader's counts both CTAs' halves
+  auto empty = [&](int s) { return smem_u32(bars + P8_MAX_STAGES + s); };      // one per CTA
+  auto sffull = [&](int s) { return smem_u32(bars + 2 * P8_MAX_STAGES + s); }; // leader's counts four warps
+  auto sfempty = [&](int s) { return smem_u32(bars + 2 * P8_MAX_STAGES + M8_SF + s); };
+  uint64_t* rest = bars + 2 * P8_MAX_STAGES + 2 * M8_SF;
+  auto tfull = [&](int a) { return smem_u32(rest + a); };
+  auto tempty = [&](int a) { return smem_u32(rest + 2 + a); };                 // leader: eight warps
+  const uint32_t drain = smem_u32(rest + 4), rawfull = smem_u32(rest + 5);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int G = cdiv(cin, 128), nchunk = cdiv(G, 4);
+  const int mtiles = cdiv(cout, 2 * M8_BM), ntiles = cdiv(tokens, N);
+  const int total = mtiles * ntiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full(s), 2);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < M8_SF; ++s) {
+      mbar_init(sffull(s), 4);
+      mbar_init(sfempty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 8);
+    }
+    mbar_init(drain, 1);
+    mbar_init(rawfull, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(holder), 512);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  pdl_wait();
+  pdl_trigger();
+  auto tile_at = [&](int it, int& mt, int& nt) {
+    if (tokens_fast) {
+      nt = it % ntiles;
+      mt = it / ntiles;
+    } else {
+      mt = it % mtiles;
+      nt = it / mtiles;
+    }
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t ph = 0, issued = 0, issued_par = 0;
+      const uint32_t full0 = mapa(full(0), 0);
+      for (int it = pair; it < total; it += npairs) {
+        int mt, nt;
+        tile_at(it, mt, nt);
+        const int wrow = mt * 2 * M8_BM + (int)rank * M8_BM, xrow = nt * N + (int)rank * (N / 2);
+        for (int g = 0; g < G; ++g) {
+          wait_through(empty(stage), ph ^ 1u, abort_flag, 411);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (ph << stage);
+          const uint32_t fbar = full0 + 8u * (uint32_t)stage;
+          mbar_expect_tx_cluster(fbar, (uint32_t)stage_bytes);
+          const uint32_t dst = smem_u32(smem + stage * stage_bytes);
+          tma_load_2d_pair(dst, &tmW, fbar, g * 128, wrow);
+          tma_load_2d_pair(dst + M8_A, &tmX, fbar, g * 128, xrow);
+          if (++stage == stages) { stage = 0; ph ^= 1u; }
+        }
+      }
+      // our copies have landed once the leader's full barrier has completed, or once our own
+      // empty barrier shows that the leader consumed them
+      for (int s = 0; s < stages; ++s)
+        if (issued & (1u << s)) mbar_wait_drain(rank == 0 ? full(s) : empty(s), (issued_par >> s) & 1u, 412);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_mx8(2 * M8_BM, N);
+      const uint64_t wd0 = sdesc(smem_u32(smem), 16, 1024), xd0 = sdesc(smem_u32(smem) + M8_A, 16, 1024);
+      int stage = 0, lt = 0;
+      uint32_t ph = 0;
+      uint32_t cc = 0;       // chunks so far, over all tiles (only its low bits and cc >= 2 matter)
+      for (int it = pair; it < total; it += npairs, ++lt) {
+        const int acc = lt & 1;
+        wait_through(tempty(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u, abort_flag, 413);
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * N);
+        for (int c = 0; c < nchunk; ++c, ++cc) {
+          const int slot = (int)(cc % M8_SF);
+          wait_through_cluster(sffull(slot), (cc / M8_SF) & 1u, abort_flag, 414);
+          if (cc >= 2) wait_through(sfempty((int)((cc - 2) % M8_SF)), ((cc - 2) / M8_SF) & 1u, abort_flag, 415);
+          tc_fence_after();
+          const uint32_t sfa = tmem + (uint32_t)(2 * N + 12 * (int)(cc & 1)), sfb = sfa + 4;
+          const uint32_t src = smem_u32(sf + slot * P8_SF_BYTES);
+          copy_scales_pair(sfa, sdesc_scales(src));
+          copy_scales_pair(sfb, sdesc_scales(src + 512));
+          if (N > 128) copy_scales_pair(sfb + 4, sdesc_scales(src + 1024));
+          const int jn = min(4, G - 4 * c);
+          for (int j = 0; j < jn; ++j) {
+            wait_through(full(stage), ph, abort_flag, 416);
+            tc_fence_after();
+            const uint64_t wd = wd0 + (uint32_t)(stage * (stage_bytes >> 4)), xd = xd0 + (uint32_t)(stage * (stage_bytes >> 4));
+            const int left = cin - (4 * c + j) * 128;
+            const uint32_t id = with_byte(idesc, j);
+            if (left >= 128) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_mx8_pair(d, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
+            } else {
+              for (int k = 0; k < left / 32; ++k) mma_mx8_pair(d, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
+            }
+            mma_commit_pair(empty(stage), 0x3);
+            if (++stage == stages) { stage = 0; ph ^= 1u; }
+          }
+          mma_commit_pair(sfempty(slot), 0x3);
+        }
+        mma_commit_pair(tfull(acc), 0x3);
+      }
+      mma_commit_pair(drain, 0x1);
+      mbar_wait_drain(drain, 0, 417);
+    }
+    __syncwarp();
+  } else if (warp >= 6) {
+    // The tile's scale bytes, N rows of G bytes one after another, come in by one bulk copy (N and
+    // so the start are multiples of 16; the up to 15 bytes behind the last whole 16 of X's scales by
+    // plain loads).  Each warp then builds its 128 tokens' words (n = 128 half + 32 j + lane) of every
+    // other chunk, up to four chunks ahead of the products, which hides the next tile's copy.
+    const int half = (warp - 6) & 1, odd = (warp - 6) >> 1;
+    const uint32_t sffull0 = mapa(sffull(0), 0);
+    uint32_t cc = 0, par = 0;
+    bool ok = true;
+    for (int it = pair; it < total && ok; it += npairs, par ^= 1u) {
+      int mt, nt;
+      tile_at(it, mt, nt);
+      const int wblock = 2 * mt + (int)rank, rows = min(N, tokens - nt * N);
+      const uint8_t* src = Xs + (size_t)nt * N * G;
+      const uint32_t bytes = (uint32_t)(rows * G), bulk = bytes & ~15u;
+      named_sync(1, 128);                      // the four warps are done with the tile before
+      if (warp == 6) {
+        if (bulk && elect_one()) {
+          mbar_expect_tx(rawfull, bulk);
+          bulk_load(smem_u32(xraw), src, bulk, rawfull);
+        }
+        if (!bulk && lane == 0) mbar_arrive(rawfull);
+        for (int i = lane; i < G; i += 32) wraw[i] = wblock * M8_BM < cout ? __ldg(Ws + (size_t)wblock * G + i) : 127;
+      } else if (warp == 7 && bulk + lane < bytes) {
+        xraw[bulk + lane] = __ldg(src + bulk + lane);
+      }
+      named_sync(1, 128);
+      ok = warp_all(mbar_wait(rawfull, par, abort_flag, 420));
+      const uint8_t* row[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = half * 128 + j * 32 + lane;
+        row[j] = n < rows ? xraw + n * G : nullptr;
+      }
+      for (int c = 0; c < nchunk && ok; ++c, ++cc) {
+        if ((int)(cc & 1u) != odd) continue;
+        const int slot = (int)(cc % M8_SF);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = row[j] ? scale_word(row[j], 4 * c, G) : 0x7f7f7f7fu;
+        const uint32_t a = half == 0 ? scale_word(wraw, 4 * c, G) : 0u;
+        ok = warp_all(mbar_wait(sfempty(slot), (cc / M8_SF + 1) & 1u, abort_flag, 418));
+        uint8_t* dst = sf + slot * P8_SF_BYTES;
+        if (half == 0) reinterpret_cast<uint4*>(dst)[lane] = make_uint4(a, a, a, a);
+        reinterpret_cast<uint4*>(dst + 512 + 512 * half)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(sffull0 + 8u * (uint32_t)slot);
+      }
+      if (!ok && warp == 6) mbar_wait_drain(rawfull, par, 421);     // nothing of ours in flight when the CTA ends
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t tempty_leader0 = mapa(tempty(0), 0), tempty_leader1 = mapa(tempty(1), 0);
+    int lt = 0;
+    for (int it = pair; it < total; it += npairs, ++lt) {
+      const int acc = lt & 1;
+      if (!warp_all(mbar_wait(tfull(acc), (uint32_t)(lt >> 1) & 1u, abort_flag, 419))) break;
+      tc_fence_after();
+      int mt, nt;
+      tile_at(it, mt, nt);
+      const int o = mt * 2 * M8_BM + (int)rank * M8_BM + q * 32 + lane;
+      const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * N);
+      const int nmax = tokens - nt * N < N ? tokens - nt * N : N;
+#pragma unroll 1
+      for (int n0 = 0; n0 < nmax; n0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(base + (uint32_t)n0, r);
+        tmem_ld_wait();
+        if (o < cout) {
+          OUT* out = Y + (size_t)(nt * N + n0) * cout + o;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (n0 + i < nmax) out[(size_t)i * cout] = from_f32<OUT>(__uint_as_float(r[i]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();   // neither CTA leaves while the other may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -287,14 +634,58 @@ lcp_status split_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, cons
                        "mm8", mW, mX, Xs, Ws, Y, cout, cin, tokens, NT, stages, S, w_early ? 1 : 0);
 }
 
+template <typename OUT>
+lcp_status pair_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, OUT* Y, int cout, int cin,
+                  int tokens, int N, cudaStream_t st) {
+  CUtensorMap mW, mX;
+  TC_TRY(make_map8(&mW, Wq, cin, cout, M8_BM, "mm8 W"));
+  TC_TRY(make_map8(&mX, Xq, cin, tokens, N / 2, "mm8 X"));
+  const int stage_bytes = M8_A + N * 64;
+  const int raw = N * cdiv(cin, 128);
+  const int fixed = M8_SF * P8_SF_BYTES + P8_MAX_G + raw + 1024 + 512;
+  int stages = (227 * 1024 - fixed) / stage_bytes;
+  if (stages > P8_MAX_STAGES) stages = P8_MAX_STAGES;
+  const int smem = stages * stage_bytes + fixed;
+  const long long total = (long long)cdiv(cout, 2 * M8_BM) * cdiv(tokens, N);
+  const int most = num_sms() / 2;
+  const int pairs = total < most ? (int)total : most;
+  TC_TRY(set_smem(mm8_pair_kernel<OUT>, smem, "mm8"));
+  return launch_kernel(mm8_pair_kernel<OUT>, dim3((unsigned)(2 * pairs)), dim3(P8_THREADS), (size_t)smem, st, 2, true,
+                       "mm8", mW, mX, Xs, Ws, Y, cout, cin, tokens, N, stages, raw, tokens <= cout ? 1 : 0);
+}
+
+// Tokens a tile of the pair kernel: the width whose rounds over the SM pairs cost least, a tile
+// costing its width and a fixed part (its fill and drain, and the W tile's share of the loads).
+int pair_width(int cout, int cin, int tokens) {
+  int best = 16;
+  long long cost = -1;
+  for (int N = 16; N <= P8_MAX_N && N * cdiv(cin, 128) <= P8_RAW; N += 16) {
+    const long long tiles = (long long)cdiv(cout, 2 * M8_BM) * cdiv(tokens, N);
+    const long long c = (tiles + num_sms() / 2 - 1) / (num_sms() / 2) * (N + 24);
+    if (cost < 0 || c <= cost) {
+      cost = c;
+      best = N;
+    }
+  }
+  return best;
+}
+
+template <typename OUT>
+lcp_status mm8_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, OUT* Y, int cout, int cin,
+                 int tokens, bool w_early, cudaStream_t st) {
+  if (tokens > 128 && cdiv(cin, 128) <= P8_MAX_G)
+    return pair_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, pair_width(cout, cin, tokens), st);
+  return split_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, w_early, st);
+}
+
 }  // namespace
 
 lcp_status tc_error_mm8(int* site, int reset) { return read_tc_error(site, reset); }
 
 lcp_status launch_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, void* Y, int cout,
                       int cin, int tokens, lcp_dtype ydt, bool w_early, cudaStream_t st) {
-  if (ydt == LCP_F32) return split_t(Xq, Xs, Wq, Ws, static_cast<float*>(Y), cout, cin, tokens, w_early, st);
-  return split_t(Xq, Xs, Wq, Ws, static_cast<__nv_bfloat16*>(Y), cout, cin, tokens, w_early, st);
+  if (ydt == LCP_F32) return mm8_t(Xq, Xs, Wq, Ws, static_cast<float*>(Y), cout, cin, tokens, w_early, st);
+  return mm8_t(Xq, Xs, Wq, Ws, static_cast<__nv_bfloat16*>(Y), cout, cin, tokens, w_early, st);
 }
 
 }  // namespace lcp
