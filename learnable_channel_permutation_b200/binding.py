@@ -9,6 +9,7 @@ library is missing, the first call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -174,22 +175,28 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     return s.cuda_stream
 
 
-class _on_device:
-    """Makes a device current for a call and restores the caller's (nothing to do on the current one)."""
+def _arg(t: Optional[torch.Tensor], dtype, index: int, name: str) -> Optional[int]:
+    """As _ptr for a call whose tensors must all lie on CUDA device ``index`` (None stays None)."""
+    if t is None:
+        return None
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{name}: every tensor must be on one CUDA device" if index >= 0 else "expected CUDA tensors")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
 
-    def __init__(self, device: torch.device):
-        self.index, self.prev = device.index, None
 
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.index:
-            self.prev = cur
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
-        return False
+def _enqueue(fn, index: int, *args, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Calls ``fn(*args, stream)`` with CUDA device ``index`` current, on its current stream unless one is given (the
+    raw handle: a Stream object costs as much as a launch)."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _enqueue(fn, index, *args, stream=stream)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if st:
+        check(st)
 
 
 def hparams(block: int, n: int, m: int, iters: int, tau: float, dtype: int, flags: int = 0) -> LcpHparams:
@@ -301,11 +308,10 @@ class _TensorList:
         self.device = device
         self.ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8, device=device)
         self.norm_out = torch.empty(1, dtype=torch.float32, device=device)
+        self.tail = (self.norm_out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
 
     def _call(self, fn, *args, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-        tail = (self.norm_out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
-        with _on_device(self.device):
-            check(fn(self.arr, self.n, *args, *tail, _stream(stream)))
+        _enqueue(fn, self.device.index, self.arr, self.n, *args, *self.tail, stream=stream)
         return self.norm_out
 
 
@@ -523,16 +529,6 @@ E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 GROUP8 = 128   # channels (and weight rows) that share a scale
 
 
-def _same_device(*tensors: Optional[torch.Tensor]) -> torch.device:
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("every tensor must be on one CUDA device")
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    return dev
-
-
 def _perm8(perm: Optional[torch.Tensor], cin: int) -> int:
     """Block size of a permutation [C_in/B, B] (0 without one)."""
     if perm is None:
@@ -542,11 +538,16 @@ def _perm8(perm: Optional[torch.Tensor], cin: int) -> int:
     return perm.shape[1]
 
 
-def _shaped(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+def _groups(n: int) -> int:
+    return (n + GROUP8 - 1) // GROUP8
+
+
+def _shaped(t: Optional[torch.Tensor], rows: int, cols: int, dtype, device, name: str) -> torch.Tensor:
+    """``t``, or a new [rows, cols] tensor when it is None."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
     return t
 
 
@@ -555,13 +556,11 @@ def quant8(X: torch.Tensor, perm: Optional[torch.Tensor] = None, Q: Optional[tor
     """8-bit activations of X [T, C_in]: values (e4m3 [T, C_in]) and scales (e8m0 [T, ceil(C_in/128)]) of
     x_pi = P_B^T x for the hard permutation perm [C_in/B, B], or of x itself."""
     T, cin = X.shape
-    B = _perm8(perm, cin)
-    dev = _same_device(X, perm, Q, S)
-    Q = _shaped(Q, (T, cin), E4M3, dev, "Q")
-    S = _shaped(S, (T, (cin + GROUP8 - 1) // GROUP8), E8M0, dev, "S")
-    with _on_device(dev):
-        check(lib().lcp_quant8(_ptr(X, None, "X"), _ptr(perm, torch.int32, "perm"), _ptr(Q, E4M3, "Q"),
-                               _ptr(S, E8M0, "S"), T, cin, B, _dt(X), _stream(None)))
+    B, dev, dt = _perm8(perm, cin), X.get_device(), _dt(X)
+    x, p = _arg(X, X.dtype, dev, "X"), _arg(perm, torch.int32, dev, "perm")
+    Q = _shaped(Q, T, cin, E4M3, X.device, "Q")
+    S = _shaped(S, T, _groups(cin), E8M0, X.device, "S")
+    _enqueue(lib().lcp_quant8, dev, x, p, _arg(Q, E4M3, dev, "Q"), _arg(S, E8M0, dev, "S"), T, cin, B, dt)
     return Q, S
 
 
@@ -571,26 +570,25 @@ def quant8_weight(W: torch.Tensor, perm: Optional[torch.Tensor] = None, mask_bit
     A = M.(W P_B) for the hard permutation perm [C_in/B, B] and the packed mask bits of any N:M pattern
     (either None: identity, nothing pruned)."""
     cout, cin = W.shape
-    B = _perm8(perm, cin)
-    dev = _same_device(W, perm, mask_bits, Q, S)
+    B, dev, dt = _perm8(perm, cin), W.get_device(), _dt(W)
+    w, p = _arg(W, W.dtype, dev, "W"), _arg(perm, torch.int32, dev, "perm")
     if mask_bits is not None and mask_bits.numel() * 32 != cout * cin:
         raise ValueError("mask_bits must be [C_out, C_in/32]")
-    Q = _shaped(Q, (cout, cin), E4M3, dev, "Q")
-    S = _shaped(S, ((cout + GROUP8 - 1) // GROUP8, (cin + GROUP8 - 1) // GROUP8), E8M0, dev, "S")
-    with _on_device(dev):
-        check(lib().lcp_quant8_weight(_ptr(W, None, "W"), _ptr(perm, torch.int32, "perm"),
-                                      _ptr(mask_bits, torch.int32, "mask"), _ptr(Q, E4M3, "Q"), _ptr(S, E8M0, "S"),
-                                      cout, cin, B, _dt(W), _stream(None)))
+    bits = _arg(mask_bits, torch.int32, dev, "mask_bits")
+    Q = _shaped(Q, cout, cin, E4M3, W.device, "Q")
+    S = _shaped(S, _groups(cout), _groups(cin), E8M0, W.device, "S")
+    _enqueue(lib().lcp_quant8_weight, dev, w, p, bits, _arg(Q, E4M3, dev, "Q"), _arg(S, E8M0, dev, "S"), cout, cin, B, dt)
     return Q, S
 
 
-def _check_weight8(Wq: torch.Tensor, Ws: torch.Tensor, cin: int) -> int:
+def _weight8(Wq: torch.Tensor, Ws: torch.Tensor, cin: int, dev: int):
+    """C_out and the addresses of an 8-bit weight for inputs of ``cin`` channels."""
     cout = Wq.shape[0]
-    if Wq.dim() != 2 or Wq.shape[1] != cin:
+    if Wq.shape != (cout, cin):
         raise ValueError(f"Wq must be [C_out, {cin}], got {tuple(Wq.shape)}")
-    if tuple(Ws.shape) != ((cout + GROUP8 - 1) // GROUP8, (cin + GROUP8 - 1) // GROUP8):
+    if Ws.shape != (_groups(cout), _groups(cin)):
         raise ValueError(f"Ws must be [ceil(C_out/128), ceil(C_in/128)], got {tuple(Ws.shape)}")
-    return cout
+    return cout, _arg(Wq, E4M3, dev, "Wq"), _arg(Ws, E8M0, dev, "Ws")
 
 
 def mm8(Xq: torch.Tensor, Xs: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, Y: Optional[torch.Tensor] = None,
@@ -598,14 +596,13 @@ def mm8(Xq: torch.Tensor, Xs: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, 
     """Y [T, C_out] = X W^T of two 8-bit operands with their scales (quant8, quant8_weight), in
     float32 or bf16 (Y's dtype when Y is given)."""
     T, cin = Xq.shape
-    cout = _check_weight8(Wq, Ws, cin)
-    if tuple(Xs.shape) != (T, (cin + GROUP8 - 1) // GROUP8):
+    dev = Xq.get_device()
+    x = _arg(Xq, E4M3, dev, "Xq")
+    if Xs.shape != (T, _groups(cin)):
         raise ValueError(f"Xs must be [T, ceil(C_in/128)], got {tuple(Xs.shape)}")
-    dev = _same_device(Xq, Xs, Wq, Ws, Y)
-    Y = _shaped(Y, (T, cout), out_dtype, dev, "Y")
-    with _on_device(dev):
-        check(lib().lcp_mm8(_ptr(Xq, E4M3, "Xq"), _ptr(Xs, E8M0, "Xs"), _ptr(Wq, E4M3, "Wq"), _ptr(Ws, E8M0, "Ws"),
-                            _ptr(Y, None, "Y"), cout, cin, T, _dt(Y), _stream(None)))
+    cout, w, ws = _weight8(Wq, Ws, cin, dev)
+    Y = _shaped(Y, T, cout, out_dtype, Xq.device, "Y")
+    _enqueue(lib().lcp_mm8, dev, x, _arg(Xs, E8M0, dev, "Xs"), w, ws, _arg(Y, Y.dtype, dev, "Y"), cout, cin, T, _dt(Y))
     return Y
 
 
@@ -616,19 +613,19 @@ def linear8(Wq: torch.Tensor, Ws: torch.Tensor, X: torch.Tensor, perm: Optional[
     permutation, then mm8.  ``workspace``: uint8, at least linear8_workspace(T, C_in) bytes (allocated
     here when None)."""
     T, cin = X.shape
-    B = _perm8(perm, cin)
-    cout = _check_weight8(Wq, Ws, cin)
-    dev = _same_device(X, Wq, Ws, perm, Y, workspace)
-    Y = _shaped(Y, (T, cout), out_dtype, dev, "Y")
+    B, dev, dt = _perm8(perm, cin), X.get_device(), _dt(X)
+    x, p = _arg(X, X.dtype, dev, "X"), _arg(perm, torch.int32, dev, "perm")
+    cout, w, ws = _weight8(Wq, Ws, cin, dev)
+    Y = _shaped(Y, T, cout, out_dtype, X.device, "Y")
     if workspace is None:
-        workspace = torch.empty(linear8_workspace(T, cin), dtype=torch.uint8, device=dev)
-    with _on_device(dev):
-        check(lib().lcp_linear8(_ptr(Wq, E4M3, "Wq"), _ptr(Ws, E8M0, "Ws"), _ptr(X, None, "X"),
-                                _ptr(perm, torch.int32, "perm"), _ptr(Y, None, "Y"), cout, cin, T, B, _dt(X), _dt(Y),
-                                _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(None)))
+        n = linear8_workspace(T, cin)
+        workspace = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=X.device)
+    _enqueue(lib().lcp_linear8, dev, w, ws, x, p, _arg(Y, Y.dtype, dev, "Y"), cout, cin, T, B, dt, _dt(Y),
+             _arg(workspace, torch.uint8, dev, "workspace"), workspace.numel())
     return Y
 
 
+@functools.lru_cache(maxsize=1024)
 def linear8_workspace(tokens: int, cin: int) -> int:
     """Bytes of workspace linear8 needs."""
     n = ctypes.c_size_t(0)

@@ -19,6 +19,8 @@
 
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "lcp_internal.cuh"
 
 namespace lcp {
@@ -30,10 +32,6 @@ constexpr int Q8_CHUNK = 256;      // channels of a warp: two scale groups, eigh
 constexpr int Q8_ROW_WARPS = 8;    // activations: warps per CTA
 constexpr int Q8_W_WARPS = 16;     // weights: warps per CTA
 constexpr int Q8_W_ROWS = 128 / Q8_W_WARPS;   // weight rows of a warp
-
-// |x| of float bits, comparable as an integer: infinities above every finite
-// value and NaNs above those.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // e8m0 byte of a block's largest magnitude.  amax = 1.f 2^(e - 127) is at most
 // 448 2^k = 1.75 2^(k + 8) for k = e - 135 when f <= .75, else for k = e - 134.
@@ -70,32 +68,64 @@ template <typename T> __device__ __forceinline__ Vec8<T> zero8() {
   return r;
 }
 
-// The slots (0 .. 255) of a lane's eight source channels in the warp's chunk;
-// -1 for a permutation entry outside [0, B).
+// The slots (0 .. 255) of a lane's eight source channels in the warp's chunk; -1 for a
+// permutation entry outside [0, B); their own places past the last channel (their zeros are
+// moved like values, so that every slot is written).
 __device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int cin, int bmask, int (&slot)[8]) {
+  int4 p[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+  if (chan < cin) {
+    p[0] = __ldg(reinterpret_cast<const int4*>(perm + chan));
+    p[1] = __ldg(reinterpret_cast<const int4*>(perm + chan) + 1);
+  }
+  const int* e = reinterpret_cast<const int*>(p);
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int p = chan + j < cin ? __ldg(perm + chan + j) : ((chan + j) & bmask);
-    if (p < 0 || p > bmask) {
-      atomicCAS(&g_quant_error, 0, 302);
-      slot[j] = -1;
-    } else {
-      slot[j] = ((chan + j) & (Q8_CHUNK - 1) & ~bmask) | p;
+    const int own = (chan + j) & (Q8_CHUNK - 1);
+    const bool out = (unsigned)e[j] > (unsigned)bmask;
+    bad |= out;
+    slot[j] = chan >= cin ? own : (out ? -1 : (own & ~bmask) | e[j]);
+  }
+  if (bad) atomicCAS(&g_quant_error, 0, 302);
+}
+// Moves two rows' eight values of every lane to their slots, through `buf` (256 words, this warp's
+// alone).  bf16: the two rows' values of a channel share a word, so one 4-byte store moves both
+// (random slots hit a bank three to four times a warp, whatever the width: half the stores
+// are half the time; 2048 x 4096, B = 64: 12.2 us with a store for each value).  float32: one
+// row after the other.
+template <typename T> __device__ __forceinline__ void permute_rows(Vec8<T>& a, Vec8<T>& b, const int (&slot)[8], uint32_t* buf, int lane) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(&a);
+    const uint32_t* y = reinterpret_cast<const uint32_t*>(&b);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (slot[j] >= 0) buf[slot[j]] = __byte_perm(x[j / 2], y[j / 2], j & 1 ? 0x7632 : 0x5410);
+    __syncwarp();
+    uint32_t w[8];
+    *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(buf + 8 * lane)[0];
+    *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(buf + 8 * lane)[1];
+    uint32_t* u = reinterpret_cast<uint32_t*>(&a);
+    uint32_t* v = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j] = __byte_perm(w[2 * j], w[2 * j + 1], 0x5410);
+      v[j] = __byte_perm(w[2 * j], w[2 * j + 1], 0x7632);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      Vec8<T>& v = r ? b : a;
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(&v);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (slot[j] >= 0) buf[slot[j]] = e[j];
+      __syncwarp();
+      v.u[0] = reinterpret_cast<const uint4*>(buf + 8 * lane)[0];
+      v.u[1] = reinterpret_cast<const uint4*>(buf + 8 * lane)[1];
     }
   }
-}
-template <typename T>
-__device__ __forceinline__ Vec8<T> permute8(const Vec8<T>& v, const int (&slot)[8], T* buf, int lane) {
-  const T* e = reinterpret_cast<const T*>(&v);
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (slot[j] >= 0) buf[slot[j]] = e[j];
-  __syncwarp();
-  Vec8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(buf + 8 * lane)[i];
-  return r;
 }
 
 template <typename T> __device__ __forceinline__ void to_f32x8(const Vec8<T>& v, float (&f)[8]) {
@@ -103,11 +133,44 @@ template <typename T> __device__ __forceinline__ void to_f32x8(const Vec8<T>& v,
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = to_f32(e[j]);
 }
-__device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
+// Largest magnitude of eight values, as float bits (infinities above every finite value and NaNs
+// above those, as integers compare).  bf16 pairs are compared as they are stored.
+__device__ __forceinline__ uint32_t amax8(const Vec8<float>& v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(f[j]));
+  for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7fffffffu);
   return m;
+}
+__device__ __forceinline__ uint32_t amax8(const Vec8<__nv_bfloat16>& v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+  return max(m << 16, m & 0xffff0000u);
+}
+// Zeroes the values whose bit of `keep` (eight bits) is clear.  bf16: a product spreads four bits
+// to the top bits of four bytes, whose signs a byte permutation then copies over a pair of values.
+__device__ __forceinline__ void apply_mask(Vec8<float>& v, uint32_t keep) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (!((keep >> j) & 1u)) w[j] = 0u;
+}
+// prmt's sign mode (which __byte_perm leaves out): selector nibble 8 + i is byte i's sign, eight times.
+template <uint32_t SEL> __device__ __forceinline__ uint32_t byte_signs(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(x), "n"(SEL));
+  return r;
+}
+__device__ __forceinline__ void apply_mask(Vec8<__nv_bfloat16>& v, uint32_t keep) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t tops = ((keep >> (4 * h)) & 15u) * 0x10204080u;
+    w[2 * h] &= byte_signs<0x9988>(tops);
+    w[2 * h + 1] &= byte_signs<0xbbaa>(tops);
+  }
 }
 // over the 16 lanes that share a scale group
 __device__ __forceinline__ uint32_t half_max(uint32_t m) {
@@ -116,42 +179,44 @@ __device__ __forceinline__ uint32_t half_max(uint32_t m) {
   return m;
 }
 
-// Activations.  A warp keeps one 256-channel chunk and walks tokens, two at a
-// time, so the permutation is read once and its slots stay in registers.
+// CTAs of the activation kernel that fit an SM.
+template <typename T, bool PERM> constexpr int row_ctas() { return sizeof(T) == 4 && PERM ? 3 : 4; }
+
+// Activations.  A warp keeps one 256-channel chunk and walks tokens two at a time, the next two
+// loading meanwhile, so the permutation is read once and its slots stay in registers.
 template <typename T, bool PERM>
-__global__ void __launch_bounds__(32 * Q8_ROW_WARPS)
+__global__ void __launch_bounds__(32 * Q8_ROW_WARPS, row_ctas<T, PERM>())
 quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, uint8_t* __restrict__ Q,
                    uint8_t* __restrict__ S, int tokens, int cin, int bmask) {
-  constexpr int UN = 2;
-  __shared__ __align__(16) T stage[PERM ? Q8_ROW_WARPS : 1][PERM ? UN : 1][PERM ? Q8_CHUNK : 8];
+  __shared__ __align__(16) uint32_t stage[PERM ? Q8_ROW_WARPS : 1][PERM ? Q8_CHUNK : 4];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
   const int G = (cin + 127) / 128;
   const bool in = chan < cin;      // C_in is a multiple of 32: a lane's channels are inside together
   pdl_wait();
   pdl_trigger();
+  const int step = gridDim.y * Q8_ROW_WARPS;
+  auto load = [&](int t) { return in && t < tokens ? load8(X + (size_t)t * cin + chan) : zero8<T>(); };
+  int t = blockIdx.y * Q8_ROW_WARPS + warp;
+  Vec8<T> next[2] = {load(t), load(t + step)};
   int slot[8];
   if (PERM) load_slots(perm, chan, cin, bmask, slot);
-  const int step = gridDim.y * Q8_ROW_WARPS;
-  for (int t0 = blockIdx.y * Q8_ROW_WARPS + warp; t0 < tokens; t0 += UN * step) {
-    Vec8<T> v[UN];
+  for (; t < tokens; t += 2 * step) {
+    Vec8<T> v[2] = {next[0], next[1]};
+    next[0] = load(t + 2 * step);
+    next[1] = load(t + 3 * step);
+    if (PERM) permute_rows(v[0], v[1], slot, stage[warp], lane);
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int t = t0 + u * step;
-      v[u] = in && t < tokens ? load8(X + (size_t)t * cin + chan) : zero8<T>();
-    }
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int t = t0 + u * step;
-      if (t >= tokens) break;        // uniform over the warp
-      if (PERM) v[u] = permute8(v[u], slot, stage[warp][u], lane);
-      float f[8];
-      to_f32x8(v[u], f);
-      const uint32_t byte = scale_byte(half_max(amax8(f)));
+    for (int u = 0; u < 2; ++u) {
+      const int row = t + u * step;
+      if (row >= tokens) break;        // uniform over the warp
+      const uint32_t byte = scale_byte(half_max(amax8(v[u])));
       const float inv = scale_inverse(byte);
       if (in) {
-        *reinterpret_cast<uint2*>(Q + (size_t)t * cin + chan) = make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
-        if ((lane & 15) == 0) S[(size_t)t * G + chan / 128] = (uint8_t)byte;
+        float f[8];
+        to_f32x8(v[u], f);
+        *reinterpret_cast<uint2*>(Q + (size_t)row * cin + chan) = make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
+        if ((lane & 15) == 0) S[(size_t)row * G + chan / 128] = (uint8_t)byte;
       }
     }
   }
@@ -161,10 +226,10 @@ quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, ui
 // and holds the values in registers (in their stored type) while the two block
 // maxima are reduced.
 template <typename T, bool PERM, bool MASK>
-__global__ void __launch_bounds__(32 * Q8_W_WARPS)
+__global__ void __launch_bounds__(32 * Q8_W_WARPS, sizeof(T) == 2 ? 2 : 1)
 quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, const uint8_t* __restrict__ mask,
                      uint8_t* __restrict__ Q, uint8_t* __restrict__ S, int cout, int cin, int bmask) {
-  __shared__ __align__(16) T stage[PERM ? Q8_W_WARPS : 1][PERM ? Q8_CHUNK : 8];
+  __shared__ __align__(16) uint32_t stage[PERM ? Q8_W_WARPS : 1][PERM ? Q8_CHUNK : 4];
   __shared__ uint32_t part[Q8_W_WARPS][2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
@@ -172,30 +237,23 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
   const bool in = chan < cin;
   pdl_wait();
   pdl_trigger();
-  int slot[8];
-  if (PERM) load_slots(perm, chan, cin, bmask, slot);
   Vec8<T> v[Q8_W_ROWS];
-  uint32_t keep[Q8_W_ROWS];
+  uint32_t keep[2] = {0u, 0u};      // a row's eight mask bits in a byte
 #pragma unroll
   for (int r = 0; r < Q8_W_ROWS; ++r) {
     const int o = blockIdx.y * 128 + r * Q8_W_WARPS + warp;
     const bool ok = in && o < cout;
     v[r] = ok ? load8(W + (size_t)o * cin + chan) : zero8<T>();
-    keep[r] = MASK && ok ? (uint32_t)__ldg(mask + (size_t)o * (cin / 8) + chan / 8) : 0xffu;
+    if (MASK && ok) keep[r / 4] |= (uint32_t)__ldg(mask + (size_t)o * (cin / 8) + chan / 8) << (8 * (r % 4));
   }
+  int slot[8];
+  if (PERM) load_slots(perm, chan, cin, bmask, slot);
   uint32_t m = 0;
 #pragma unroll
   for (int r = 0; r < Q8_W_ROWS; ++r) {
-    if (PERM) v[r] = permute8(v[r], slot, stage[warp], lane);
-    if (MASK) {
-      T* e = reinterpret_cast<T*>(&v[r]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (!((keep[r] >> j) & 1u)) e[j] = from_f32<T>(0.f);
-    }
-    float f[8];
-    to_f32x8(v[r], f);
-    m = max(m, amax8(f));
+    if (PERM && r % 2 == 0) permute_rows(v[r], v[r + 1], slot, stage[warp], lane);
+    if (MASK) apply_mask(v[r], keep[r / 4] >> (8 * (r % 4)));
+    m = max(m, amax8(v[r]));
   }
   m = half_max(m);
   if ((lane & 15) == 0) part[warp][lane >> 4] = m;
@@ -225,11 +283,9 @@ lcp_status rows_t(const T* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int t
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int chunks = cdiv_host(cin, Q8_CHUNK);
-  // enough CTAs for two rounds of eight on every SM, each warp walking the rest of the tokens
-  int gy = cdiv_host(tokens, Q8_ROW_WARPS);
-  const int most = cdiv_host(16 * sms, chunks);
-  if (gy > most) gy = most;
-  if (gy > 65535) gy = 65535;
+  // as many CTAs as fit the GPU at once (one more would cost a second round of all of them)
+  const int fit = (perm ? row_ctas<T, true>() : row_ctas<T, false>()) * sms / chunks;
+  const int gy = std::min(cdiv_host(tokens, Q8_ROW_WARPS), std::max(fit, 1));
   const dim3 grid((unsigned)chunks, (unsigned)gy);
   const int bmask = perm ? B - 1 : 0;
   if (perm)
