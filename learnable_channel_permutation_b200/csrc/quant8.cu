@@ -68,39 +68,44 @@ template <typename T> __device__ __forceinline__ Vec8<T> zero8() {
   return r;
 }
 
-// The slots (0 .. 255) of a lane's eight source channels in the warp's chunk; -1 for a
-// permutation entry outside [0, B); their own places past the last channel (their zeros are
-// moved like values, so that every slot is written).
-__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int cin, int bmask, int (&slot)[8]) {
+constexpr int Q8_STAGE = Q8_CHUNK + 4;   // words of a warp's exchange buffer; word 256 takes what has no slot
+
+// Where a lane's eight source channels of the warp's chunk go in the exchange buffer (shared
+// addresses): word 256 for a permutation entry outside [0, B); their own places past the last
+// channel (their zeros are moved like values, so that every slot is written).
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int cin, int bmask,
+                                           const uint32_t* buf, uint32_t (&slot)[8]) {
   int4 p[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
   if (chan < cin) {
     p[0] = __ldg(reinterpret_cast<const int4*>(perm + chan));
     p[1] = __ldg(reinterpret_cast<const int4*>(perm + chan) + 1);
   }
   const int* e = reinterpret_cast<const int*>(p);
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(buf));
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int own = (chan + j) & (Q8_CHUNK - 1);
     const bool out = (unsigned)e[j] > (unsigned)bmask;
     bad |= out;
-    slot[j] = chan >= cin ? own : (out ? -1 : (own & ~bmask) | e[j]);
+    slot[j] = base + 4u * (uint32_t)(chan >= cin ? own : (out ? Q8_CHUNK : (own & ~bmask) | e[j]));
   }
   if (bad) atomicCAS(&g_quant_error, 0, 302);
 }
-// Moves two rows' eight values of every lane to their slots, through `buf` (256 words, this warp's
-// alone).  bf16: the two rows' values of a channel share a word, so one 4-byte store moves both
-// (random slots hit a bank three to four times a warp, whatever the width: half the stores
-// are half the time; 2048 x 4096, B = 64: 12.2 us with a store for each value).  float32: one
-// row after the other.
-template <typename T> __device__ __forceinline__ void permute_rows(Vec8<T>& a, Vec8<T>& b, const int (&slot)[8], uint32_t* buf, int lane) {
+__device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+// Moves two rows' eight values of every lane to their slots, through `buf` (this warp's alone).
+// bf16: the two rows' values of a channel share a word, so one 4-byte store moves both
+// (random slots hit a bank three to four times a warp, whatever the width).  float32: one row
+// after the other.
+template <typename T> __device__ __forceinline__ void permute_rows(Vec8<T>& a, Vec8<T>& b, const uint32_t (&slot)[8], const uint32_t* buf, int lane) {
   if constexpr (sizeof(T) == 2) {
     const uint32_t* x = reinterpret_cast<const uint32_t*>(&a);
     const uint32_t* y = reinterpret_cast<const uint32_t*>(&b);
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (slot[j] >= 0) buf[slot[j]] = __byte_perm(x[j / 2], y[j / 2], j & 1 ? 0x7632 : 0x5410);
+    for (int j = 0; j < 8; ++j) st_shared(slot[j], __byte_perm(x[j / 2], y[j / 2], j & 1 ? 0x7632 : 0x5410));
     __syncwarp();
     uint32_t w[8];
     *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(buf + 8 * lane)[0];
@@ -119,8 +124,7 @@ template <typename T> __device__ __forceinline__ void permute_rows(Vec8<T>& a, V
       const uint32_t* e = reinterpret_cast<const uint32_t*>(&v);
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (slot[j] >= 0) buf[slot[j]] = e[j];
+      for (int j = 0; j < 8; ++j) st_shared(slot[j], e[j]);
       __syncwarp();
       v.u[0] = reinterpret_cast<const uint4*>(buf + 8 * lane)[0];
       v.u[1] = reinterpret_cast<const uint4*>(buf + 8 * lane)[1];
@@ -128,11 +132,6 @@ template <typename T> __device__ __forceinline__ void permute_rows(Vec8<T>& a, V
   }
 }
 
-template <typename T> __device__ __forceinline__ void to_f32x8(const Vec8<T>& v, float (&f)[8]) {
-  const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = to_f32(e[j]);
-}
 // Largest magnitude of eight values, as float bits (infinities above every finite value and NaNs
 // above those, as integers compare).  bf16 pairs are compared as they are stored.
 __device__ __forceinline__ uint32_t amax8(const Vec8<float>& v) {
@@ -142,11 +141,21 @@ __device__ __forceinline__ uint32_t amax8(const Vec8<float>& v) {
   for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7fffffffu);
   return m;
 }
-__device__ __forceinline__ uint32_t amax8(const Vec8<__nv_bfloat16>& v) {
+// a bf16 pair's maxima; a NaN wins
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t amax_pair(const Vec8<__nv_bfloat16>& v) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-  uint32_t m = 0;
+  uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+  for (int j = 1; j < 4; ++j) m = max_pair(m, w[j] & 0x7fff7fffu);
+  return m;
+}
+__device__ __forceinline__ uint32_t amax8(const Vec8<__nv_bfloat16>& v) {
+  const uint32_t m = amax_pair(v);
   return max(m << 16, m & 0xffff0000u);
 }
 // Zeroes the values whose bit of `keep` (eight bits) is clear.  bf16: a product spreads four bits
@@ -178,6 +187,37 @@ __device__ __forceinline__ uint32_t half_max(uint32_t m) {
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
+// The group maxima of two rows (bf16: both travel in one word).
+__device__ __forceinline__ void group_max(const Vec8<float> (&v)[2], uint32_t (&m)[2]) {
+  m[0] = half_max(amax8(v[0]));
+  m[1] = half_max(amax8(v[1]));
+}
+__device__ __forceinline__ void group_max(const Vec8<__nv_bfloat16> (&v)[2], uint32_t (&m)[2]) {
+  const uint32_t a = amax_pair(v[0]), b = amax_pair(v[1]);
+  uint32_t w = max_pair(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) w = max_pair(w, __shfl_xor_sync(0xffffffffu, w, o));
+  m[0] = w << 16;
+  m[1] = w & 0xffff0000u;
+}
+
+// Eight values times a power of two, as e4m3.  In bf16 the product is exact too (a result below
+// bf16's range is far below e4m3's).
+__device__ __forceinline__ uint2 to_e4m3(const Vec8<float>& v, float inv) {
+  const float* f = reinterpret_cast<const float*>(&v);
+  return make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
+}
+__device__ __forceinline__ uint32_t pair_e4m3(uint32_t w, __nv_bfloat162 inv) {
+  const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), inv);
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&p);
+  return __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), __NV_SATFINITE,
+                                  __NV_E4M3);
+}
+__device__ __forceinline__ uint2 to_e4m3(const Vec8<__nv_bfloat16>& v, float inv) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+  const __nv_bfloat162 i2 = __float2bfloat162_rn(inv);
+  return make_uint2(pair_e4m3(w[0], i2) | (pair_e4m3(w[1], i2) << 16), pair_e4m3(w[2], i2) | (pair_e4m3(w[3], i2) << 16));
+}
 
 // CTAs of the activation kernel that fit an SM.
 template <typename T, bool PERM> constexpr int row_ctas() { return sizeof(T) == 4 && PERM ? 3 : 4; }
@@ -188,7 +228,7 @@ template <typename T, bool PERM>
 __global__ void __launch_bounds__(32 * Q8_ROW_WARPS, row_ctas<T, PERM>())
 quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, uint8_t* __restrict__ Q,
                    uint8_t* __restrict__ S, int tokens, int cin, int bmask) {
-  __shared__ __align__(16) uint32_t stage[PERM ? Q8_ROW_WARPS : 1][PERM ? Q8_CHUNK : 4];
+  __shared__ __align__(16) uint32_t stage[PERM ? Q8_ROW_WARPS : 1][PERM ? Q8_STAGE : 4];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
   const int G = (cin + 127) / 128;
@@ -199,25 +239,22 @@ quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, ui
   auto load = [&](int t) { return in && t < tokens ? load8(X + (size_t)t * cin + chan) : zero8<T>(); };
   int t = blockIdx.y * Q8_ROW_WARPS + warp;
   Vec8<T> next[2] = {load(t), load(t + step)};
-  int slot[8];
-  if (PERM) load_slots(perm, chan, cin, bmask, slot);
+  uint32_t slot[8];
+  if (PERM) load_slots(perm, chan, cin, bmask, stage[warp], slot);
   for (; t < tokens; t += 2 * step) {
     Vec8<T> v[2] = {next[0], next[1]};
     next[0] = load(t + 2 * step);
     next[1] = load(t + 3 * step);
     if (PERM) permute_rows(v[0], v[1], slot, stage[warp], lane);
+    uint32_t m[2];
+    group_max(v, m);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int row = t + u * step;
-      if (row >= tokens) break;        // uniform over the warp
-      const uint32_t byte = scale_byte(half_max(amax8(v[u])));
-      const float inv = scale_inverse(byte);
-      if (in) {
-        float f[8];
-        to_f32x8(v[u], f);
-        *reinterpret_cast<uint2*>(Q + (size_t)row * cin + chan) = make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
-        if ((lane & 15) == 0) S[(size_t)row * G + chan / 128] = (uint8_t)byte;
-      }
+      if (row >= tokens || !in) break;
+      const uint32_t byte = scale_byte(m[u]);
+      *reinterpret_cast<uint2*>(Q + (size_t)row * cin + chan) = to_e4m3(v[u], scale_inverse(byte));
+      if ((lane & 15) == 0) S[(size_t)row * G + chan / 128] = (uint8_t)byte;
     }
   }
 }
@@ -229,7 +266,7 @@ template <typename T, bool PERM, bool MASK>
 __global__ void __launch_bounds__(32 * Q8_W_WARPS, sizeof(T) == 2 ? 2 : 1)
 quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, const uint8_t* __restrict__ mask,
                      uint8_t* __restrict__ Q, uint8_t* __restrict__ S, int cout, int cin, int bmask) {
-  __shared__ __align__(16) uint32_t stage[PERM ? Q8_W_WARPS : 1][PERM ? Q8_CHUNK : 4];
+  __shared__ __align__(16) uint32_t stage[PERM ? Q8_W_WARPS : 1][PERM ? Q8_STAGE : 4];
   __shared__ uint32_t part[Q8_W_WARPS][2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
@@ -246,8 +283,8 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
     v[r] = ok ? load8(W + (size_t)o * cin + chan) : zero8<T>();
     if (MASK && ok) keep[r / 4] |= (uint32_t)__ldg(mask + (size_t)o * (cin / 8) + chan / 8) << (8 * (r % 4));
   }
-  int slot[8];
-  if (PERM) load_slots(perm, chan, cin, bmask, slot);
+  uint32_t slot[8];
+  if (PERM) load_slots(perm, chan, cin, bmask, stage[warp], slot);
   uint32_t m = 0;
 #pragma unroll
   for (int r = 0; r < Q8_W_ROWS; ++r) {
@@ -268,9 +305,7 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
   for (int r = 0; r < Q8_W_ROWS; ++r) {
     const int o = blockIdx.y * 128 + r * Q8_W_WARPS + warp;
     if (o >= cout) break;
-    float f[8];
-    to_f32x8(v[r], f);
-    *reinterpret_cast<uint2*>(Q + (size_t)o * cin + chan) = make_uint2(pack4_e4m3(f, inv), pack4_e4m3(f + 4, inv));
+    *reinterpret_cast<uint2*>(Q + (size_t)o * cin + chan) = to_e4m3(v[r], inv);
   }
   if (warp == 0 && (lane & 15) == 0) S[(size_t)blockIdx.y * G + chan / 128] = (uint8_t)byte;
 }
