@@ -19,7 +19,9 @@
 // the norm adds the partials in a fixed order in every CTA, so the result does
 // not depend on timing and the workspace holds nothing that has to be cleared.
 // The second pass walks the chunks backwards: the end of the list is what the
-// first pass left in L2.
+// first pass left in L2.  Everything but those kKeep bytes is read and written
+// with streaming accesses, so that it stays there (a 7B model's logits, 291 MB:
+// 143 us without, 138 with 64 to 80 MB kept, 140 with 112).
 
 #include <type_traits>
 
@@ -31,6 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 8192;      // values of a chunk
 constexpr double kClipEps = 1e-6;
+constexpr long long kKeep = 80LL << 20;   // bytes of the list's end that the first pass leaves in L2
 
 // The tensors of one launch, in its parameters: nothing is copied to the device
 // before the launch and a captured graph holds its own list.  The capacity is
@@ -86,7 +89,7 @@ __device__ __forceinline__ double sq(float x) { return (double)x * (double)x; }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <typename T> __device__ __forceinline__ double chunk_squares(const T* p, int n) {
+template <typename T> __device__ __forceinline__ double chunk_squares(const T* p, int n, bool stream) {
   constexpr int V = 16 / sizeof(T);
   double s0 = 0.0, s1 = 0.0;
   int head = head_of<sizeof(T)>(p);
@@ -95,7 +98,7 @@ template <typename T> __device__ __forceinline__ double chunk_squares(const T* p
   const uint4* q = reinterpret_cast<const uint4*>(p + head);
 #pragma unroll 4
   for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    const uint4 u = __ldg(q + i);
+    const uint4 u = stream ? __ldcs(q + i) : __ldg(q + i);
     if constexpr (sizeof(T) == 4) {
       s0 += sq(__uint_as_float(u.x)) + sq(__uint_as_float(u.y));
       s1 += sq(__uint_as_float(u.z)) + sq(__uint_as_float(u.w));
@@ -117,7 +120,7 @@ template <int CAP> struct is_adam<AdamTable<CAP>> { static constexpr bool value 
 
 template <typename Table>
 __global__ void __launch_bounds__(kThreads)
-squares_kernel(const __grid_constant__ Table t, double* __restrict__ partials) {
+squares_kernel(const __grid_constant__ Table t, double* __restrict__ partials, long long keep) {
   pdl_wait();
   pdl_trigger();
   double s = 0.0;
@@ -128,8 +131,9 @@ squares_kernel(const __grid_constant__ Table t, double* __restrict__ partials) {
     const int n = (int)(t.n[i] - at < kChunk ? t.n[i] - at : kChunk);
     bool bf = false;
     if constexpr (!is_adam<Table>::value) bf = t.bf16[i];
-    if (bf) s += chunk_squares(reinterpret_cast<const __nv_bfloat16*>(t.g[i]) + at, n);
-    else s += chunk_squares(reinterpret_cast<const float*>(t.g[i]) + at, n);
+    const bool stream = (long long)(chunks - c) * kChunk * (bf ? 2 : 4) > keep;
+    if (bf) s += chunk_squares(reinterpret_cast<const __nv_bfloat16*>(t.g[i]) + at, n, stream);
+    else s += chunk_squares(reinterpret_cast<const float*>(t.g[i]) + at, n, stream);
   }
   s = block_sum(s);
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
@@ -173,7 +177,7 @@ template <typename T> __device__ __forceinline__ void chunk_scale(const T* g, T*
   uint4* w = reinterpret_cast<uint4*>(out + head);
 #pragma unroll 4
   for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    uint4 u = q[i];
+    uint4 u = __ldcs(q + i);
     if constexpr (sizeof(T) == 4) {
       u.x = __float_as_uint(__uint_as_float(u.x) * f);
       u.y = __float_as_uint(__uint_as_float(u.y) * f);
@@ -185,7 +189,7 @@ template <typename T> __device__ __forceinline__ void chunk_scale(const T* g, T*
       u.z = scale_pair(u.z, f);
       u.w = scale_pair(u.w, f);
     }
-    w[i] = u;
+    __stcs(w + i, u);
   }
   const int rest = n - vecs * V;
   if ((int)threadIdx.x < rest) {
@@ -239,17 +243,17 @@ adamw_list_kernel(const __grid_constant__ AdamTable<CAP> t, const double* __rest
     const int vecs = (n - head) / 4;
 #pragma unroll 2
     for (int q = threadIdx.x; q < vecs; q += kThreads) {
-      float4 l4 = reinterpret_cast<float4*>(L + head)[q];
-      float4 g4 = reinterpret_cast<const float4*>(g + head)[q];
-      float4 m4 = reinterpret_cast<float4*>(m + head)[q];
-      float4 v4 = reinterpret_cast<float4*>(w + head)[q];
+      float4 l4 = __ldcs(reinterpret_cast<float4*>(L + head) + q);
+      float4 g4 = __ldcs(reinterpret_cast<const float4*>(g + head) + q);
+      float4 m4 = __ldcs(reinterpret_cast<float4*>(m + head) + q);
+      float4 v4 = __ldcs(reinterpret_cast<float4*>(w + head) + q);
       adam1(l4.x, g4.x * f, m4.x, v4.x, c);
       adam1(l4.y, g4.y * f, m4.y, v4.y, c);
       adam1(l4.z, g4.z * f, m4.z, v4.z, c);
       adam1(l4.w, g4.w * f, m4.w, v4.w, c);
-      reinterpret_cast<float4*>(L + head)[q] = l4;
-      reinterpret_cast<float4*>(m + head)[q] = m4;
-      reinterpret_cast<float4*>(w + head)[q] = v4;
+      __stcs(reinterpret_cast<float4*>(L + head) + q, l4);
+      __stcs(reinterpret_cast<float4*>(m + head) + q, m4);
+      __stcs(reinterpret_cast<float4*>(w + head) + q, v4);
     }
     for (int r = threadIdx.x; r < n - vecs * 4; r += kThreads) {
       const int e = r < head ? r : r + vecs * 4;
@@ -348,7 +352,7 @@ lcp_status squares(const Desc* d, int count, double* partials, int* np, cudaStre
   return each_table<Table, Small>(d, count, [&](const auto& t, int grid) {
     using T = std::decay_t<decltype(t)>;
     const lcp_status r = launch_kernel(squares_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1, true, "grad_norm",
-                                       t, partials + *np);
+                                       t, partials + *np, kKeep);
     *np += grid;
     return r;
   });

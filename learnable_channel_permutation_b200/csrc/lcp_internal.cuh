@@ -258,7 +258,8 @@ lcp_status launch_score(const void* W, const void* X, void* S, float* stats, int
                         lcp_dtype dt, cudaStream_t st);
 
 // AdamW of one value (adamw.cu): c holds every coefficient, formed in double and
-// rounded once.
+// rounded once.  Every fused multiply-add is written out, so that all kernels that
+// use it give the same bits.
 struct AdamCoef {
   float b1, b2, c1, c2, eps, decay;   // c = 1 - b, decay = 1 - lr wd
   float step;                 // lr / (1 - b1^t)
@@ -266,9 +267,9 @@ struct AdamCoef {
 };
 AdamCoef adam_coef(double lr, double beta1, double beta2, double eps, double weight_decay, int t);
 __device__ __forceinline__ void adam1(float& L, float g, float& m, float& v, const AdamCoef& c) {
-  m = c.b1 * m + c.c1 * g;
-  v = c.b2 * v + c.c2 * g * g;
-  L = L * c.decay - c.step * m / (sqrtf(v) * c.inv_sqrt_bc2 + c.eps);
+  m = fmaf(c.c1, g, __fmul_rn(c.b1, m));
+  v = fmaf(__fmul_rn(c.c2, g), g, __fmul_rn(c.b2, v));
+  L = fmaf(L, c.decay, -(__fmul_rn(c.step, m) / fmaf(sqrtf(v), c.inv_sqrt_bc2, c.eps)));
 }
 
 // The gradient norm over a list of tensors, clipping by it, and one AdamW update of a
