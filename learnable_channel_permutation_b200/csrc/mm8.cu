@@ -113,6 +113,7 @@ constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one sca
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
 constexpr int M8_THREADS = 224;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6: scales
 constexpr int M8_MAX_STAGES = 8;
+constexpr int M8_SETS = 4;            // sets of scales in tensor memory
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
   float4 v;
@@ -139,8 +140,8 @@ template <typename OUT> __device__ __forceinline__ void store4(OUT* out, const f
 //
 // Scale words: a chunk is four groups, so a row's four scale bytes are one 32-bit word and
 // the instruction picks the byte of the group at hand.  Warp 6 builds the words of chunk c in
-// ring slot c % 4; the MMA thread copies them to tensor-memory set c % 2 and, before it does,
-// waits for the products of chunk c - 2 that read that set.
+// ring slot c % 4 once the products of chunk c - 4 are done, and the MMA thread copies them to
+// the tensor-memory set of the same number, which those products were the last to read.
 template <typename OUT>
 __global__ void __launch_bounds__(M8_THREADS)
 mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -152,6 +153,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   uint8_t* sf = smem + stages * stage_bytes;                  // M8_SF x (512 B of W, 512 B of X)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sf + M8_SF * 1024);
   uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * M8_MAX_STAGES + 2 * M8_SF + 1);
+  static_assert(M8_SETS == M8_SF, "a ring slot and a set are both free when the same products are done");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
   auto full = [&](int s) { return smem_u32(bars + s); };
   auto empty = [&](int s) { return smem_u32(bars + M8_MAX_STAGES + s); };
@@ -168,9 +170,9 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);   // never empty: S <= G
   const int nk = g1 - g0, nchunk = cdiv(nk, 4);
 
-  // accumulator columns [0, NT), then two sets of (4 columns of W scales, 4 of X scales)
+  // accumulator columns [0, NT), then M8_SETS sets of (4 columns of W scales, 4 of X scales)
   uint32_t ncols = 32;
-  while ((int)ncols < NT + 16) ncols *= 2;
+  while ((int)ncols < NT + 8 * M8_SETS) ncols *= 2;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -228,9 +230,8 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       for (int c = 0; c < nchunk; ++c) {
         const int slot = c % M8_SF;
         wait_through(sffull(slot), (uint32_t)(c / M8_SF) & 1u, abort_flag, 403);
-        if (c >= 2) wait_through(sfempty((c - 2) % M8_SF), (uint32_t)((c - 2) / M8_SF) & 1u, abort_flag, 404);
         tc_fence_after();
-        const uint32_t sfa = tmem + (uint32_t)(NT + 8 * (c & 1)), sfb = sfa + 4;
+        const uint32_t sfa = tmem + (uint32_t)(NT + 8 * slot), sfb = sfa + 4;
         copy_scales(sfa, sdesc_scales(smem_u32(sf + slot * 1024)));
         copy_scales(sfb, sdesc_scales(smem_u32(sf + slot * 1024 + 512)));
         const int jn = min(4, nk - 4 * c);
@@ -362,9 +363,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // Each CTA stages its 128 rows of W and its half of the tile's tokens, the leader issues
 // M = 256 products over both, and each CTA keeps its 128 channels x N tokens of the result in one
 // of two accumulators, so the next tile's products run while the epilogue stores this one.
-// Columns: two accumulators of N, then two sets of scales (4 of W, 8 of X): N <= 240.
-constexpr int P8_THREADS = 320;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6-9: scales (128 tokens, every other chunk)
+// Columns: two accumulators of N, then the sets of scales (4 of W, 8 of X): two at the least, so N <= 240.
+constexpr int P8_THREADS = 320;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6-9: scales (128 tokens, every other slot)
 constexpr int P8_SF_BYTES = 1536;     // a chunk's scale words: 512 B of W, 2 x 512 B of X
+constexpr int P8_SLOT = 4;            // chunks of a ring slot: one hand-over between the CTAs for 16 groups
+constexpr int P8_SLOTS = 2;
+constexpr int P8_MAX_SETS = 8;        // sets of scales in tensor memory: as many as fit beside the accumulators
 constexpr int P8_MAX_N = 240;
 constexpr int P8_MAX_G = 256;         // C_in <= 32768: a tile's scale bytes are staged whole
 constexpr int P8_RAW = 40 * 1024;     // their room at most: N G <= 40 KB
@@ -379,19 +383,20 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   uint8_t* smem = align1024(smem_raw);
   const int stage_bytes = M8_A + N * 64;
   uint8_t* sf = smem + stages * stage_bytes;
-  uint8_t* wraw = sf + M8_SF * P8_SF_BYTES;      // the tile's W scales (one row), then its X scales (N rows)
+  uint8_t* wraw = sf + P8_SLOTS * P8_SLOT * P8_SF_BYTES;      // the tile's W scales (one row), then its X scales (N rows)
   uint8_t* xraw = wraw + P8_MAX_G;
   uint64_t* bars = reinterpret_cast<uint64_t*>(xraw + raw_bytes);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * P8_MAX_STAGES + 2 * M8_SF + 6);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * P8_MAX_STAGES + 2 * P8_SLOTS + 6 + P8_MAX_SETS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
   auto full = [&](int s) { return smem_u32(bars + s); };                       // leader's counts both CTAs' halves
   auto empty = [&](int s) { return smem_u32(bars + P8_MAX_STAGES + s); };      // one per CTA
   auto sffull = [&](int s) { return smem_u32(bars + 2 * P8_MAX_STAGES + s); }; // leader's counts four warps
-  auto sfempty = [&](int s) { return smem_u32(bars + 2 * P8_MAX_STAGES + M8_SF + s); };
-  uint64_t* rest = bars + 2 * P8_MAX_STAGES + 2 * M8_SF;
+  auto sfempty = [&](int s) { return smem_u32(bars + 2 * P8_MAX_STAGES + P8_SLOTS + s); };
+  uint64_t* rest = bars + 2 * P8_MAX_STAGES + 2 * P8_SLOTS;
   auto tfull = [&](int a) { return smem_u32(rest + a); };
   auto tempty = [&](int a) { return smem_u32(rest + 2 + a); };                 // leader: eight warps
   const uint32_t drain = smem_u32(rest + 4), rawfull = smem_u32(rest + 5);
+  auto setfree = [&](int a) { return smem_u32(rest + 6 + a); };                // leader: a set of scales in tensor memory
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -405,10 +410,11 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       mbar_init(full(s), 2);
       mbar_init(empty(s), 1);
     }
-    for (int s = 0; s < M8_SF; ++s) {
+    for (int s = 0; s < P8_SLOTS; ++s) {
       mbar_init(sffull(s), 4);
       mbar_init(sfempty(s), 1);
     }
+    for (int a = 0; a < P8_MAX_SETS; ++a) mbar_init(setfree(a), 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
       mbar_init(tempty(a), 8);
@@ -468,19 +474,21 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       const uint64_t wd0 = sdesc(smem_u32(smem), 16, 1024), xd0 = sdesc(smem_u32(smem) + M8_A, 16, 1024);
       int stage = 0, lt = 0;
       uint32_t ph = 0;
-      uint32_t cc = 0;       // chunks so far, over all tiles (only its low bits and cc >= 2 matter)
+      const int sets = min(P8_MAX_SETS, (512 - 2 * N) / 12);
+      int set = 0;
+      uint32_t sph = 1, ss = 0;     // parity of the set's last use; ring slots so far, over all tiles
       for (int it = pair; it < total; it += npairs, ++lt) {
         const int acc = lt & 1;
         wait_through(tempty(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u, abort_flag, 413);
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * N);
-        for (int c = 0; c < nchunk; ++c, ++cc) {
-          const int slot = (int)(cc % M8_SF);
-          wait_through_cluster(sffull(slot), (cc / M8_SF) & 1u, abort_flag, 414);
-          if (cc >= 2) wait_through(sfempty((int)((cc - 2) % M8_SF)), ((cc - 2) / M8_SF) & 1u, abort_flag, 415);
+        for (int c = 0; c < nchunk; ++c) {
+          const int slot = (int)(ss % P8_SLOTS);
+          if (c % P8_SLOT == 0) wait_through_cluster(sffull(slot), (ss / P8_SLOTS) & 1u, abort_flag, 414);
+          wait_through(setfree(set), sph, abort_flag, 415);     // the products that read this set last
           tc_fence_after();
-          const uint32_t sfa = tmem + (uint32_t)(2 * N + 12 * (int)(cc & 1)), sfb = sfa + 4;
-          const uint32_t src = smem_u32(sf + slot * P8_SF_BYTES);
+          const uint32_t sfa = tmem + (uint32_t)(2 * N + 12 * set), sfb = sfa + 4;
+          const uint32_t src = smem_u32(sf + (slot * P8_SLOT + c % P8_SLOT) * P8_SF_BYTES);
           copy_scales_pair(sfa, sdesc_scales(src));
           copy_scales_pair(sfb, sdesc_scales(src + 512));
           if (N > 128) copy_scales_pair(sfb + 4, sdesc_scales(src + 1024));
@@ -500,7 +508,12 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             mma_commit_pair(empty(stage), 0x3);
             if (++stage == stages) { stage = 0; ph ^= 1u; }
           }
-          mma_commit_pair(sfempty(slot), 0x3);
+          mma_commit_pair(setfree(set), 0x1);
+          if (++set == sets) { set = 0; sph ^= 1u; }
+          if (c % P8_SLOT == P8_SLOT - 1 || c == nchunk - 1) {
+            mma_commit_pair(sfempty(slot), 0x3);
+            ++ss;
+          }
         }
         mma_commit_pair(tfull(acc), 0x3);
       }
@@ -512,10 +525,10 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     // The tile's scale bytes, N rows of G bytes one after another, come in by one bulk copy (N and
     // so the start are multiples of 16; the up to 15 bytes behind the last whole 16 of X's scales by
     // plain loads).  Each warp then builds its 128 tokens' words (n = 128 half + 32 j + lane) of every
-    // other chunk, up to four chunks ahead of the products, which hides the next tile's copy.
+    // other ring slot, ahead of the products, which hides the next tile's copy.
     const int half = (warp - 6) & 1, odd = (warp - 6) >> 1;
     const uint32_t sffull0 = mapa(sffull(0), 0);
-    uint32_t cc = 0, par = 0;
+    uint32_t ss = 0, par = 0;
     bool ok = true;
     for (int it = pair; it < total && ok; it += npairs, par ^= 1u) {
       int mt, nt;
@@ -542,17 +555,25 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const int n = half * 128 + j * 32 + lane;
         row[j] = n < rows ? xraw + n * G : nullptr;
       }
-      for (int c = 0; c < nchunk && ok; ++c, ++cc) {
-        if ((int)(cc & 1u) != odd) continue;
-        const int slot = (int)(cc % M8_SF);
-        uint32_t w[4];
+      for (int c0 = 0; c0 < nchunk && ok; c0 += P8_SLOT, ++ss) {
+        if ((int)(ss & 1u) != odd) continue;
+        const int slot = (int)(ss % P8_SLOTS);
+        ok = warp_all(mbar_wait(sfempty(slot), (ss / P8_SLOTS + 1) & 1u, abort_flag, 418));
+        if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = row[j] ? scale_word(row[j], 4 * c, G) : 0x7f7f7f7fu;
-        const uint32_t a = half == 0 ? scale_word(wraw, 4 * c, G) : 0u;
-        ok = warp_all(mbar_wait(sfempty(slot), (cc / M8_SF + 1) & 1u, abort_flag, 418));
-        uint8_t* dst = sf + slot * P8_SF_BYTES;
-        if (half == 0) reinterpret_cast<uint4*>(dst)[lane] = make_uint4(a, a, a, a);
-        reinterpret_cast<uint4*>(dst + 512 + 512 * half)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < P8_SLOT; ++i) {
+          const int c = c0 + i;
+          if (c >= nchunk) break;
+          uint8_t* dst = sf + (slot * P8_SLOT + i) * P8_SF_BYTES;
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = row[j] ? scale_word(row[j], 4 * c, G) : 0x7f7f7f7fu;
+          reinterpret_cast<uint4*>(dst + 512 + 512 * half)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (half == 0) {
+            const uint32_t a = scale_word(wraw, 4 * c, G);
+            reinterpret_cast<uint4*>(dst)[lane] = make_uint4(a, a, a, a);
+          }
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_release_cluster(sffull0 + 8u * (uint32_t)slot);
@@ -572,17 +593,32 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       const int o = mt * 2 * M8_BM + (int)rank * M8_BM + q * 32 + lane;
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * N);
       const int nmax = tokens - nt * N < N ? tokens - nt * N : N;
-#pragma unroll 1
-      for (int n0 = 0; n0 < nmax; n0 += 16) {
-        uint32_t r[16];
-        tmem_ld16(base + (uint32_t)n0, r);
-        tmem_ld_wait();
+      // 16 tokens a step; the next step's accumulators are on their way while this one's are stored
+      OUT* out = Y + (size_t)nt * N * cout + o;
+      auto store16 = [&](const uint32_t(&r)[16], int n0) {
         if (o < cout) {
-          OUT* out = Y + (size_t)(nt * N + n0) * cout + o;
+          if (n0 + 16 <= nmax) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (n0 + i < nmax) out[(size_t)i * cout] = from_f32<OUT>(__uint_as_float(r[i]));
+            for (int i = 0; i < 16; ++i) out[(size_t)i * cout] = from_f32<OUT>(__uint_as_float(r[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (n0 + i < nmax) out[(size_t)i * cout] = from_f32<OUT>(__uint_as_float(r[i]));
+          }
         }
+        out += 16 * (size_t)cout;
+      };
+      uint32_t ra[16], rb[16];
+      tmem_ld16(base, ra);
+#pragma unroll 1
+      for (int n0 = 0; n0 < nmax; n0 += 32) {
+        tmem_ld_wait();
+        if (n0 + 16 < nmax) tmem_ld16(base + (uint32_t)(n0 + 16), rb);
+        store16(ra, n0);
+        if (n0 + 16 >= nmax) break;
+        tmem_ld_wait();
+        if (n0 + 32 < nmax) tmem_ld16(base + (uint32_t)(n0 + 32), ra);
+        store16(rb, n0 + 16);
       }
       tc_fence_before();
       __syncwarp();
@@ -642,7 +678,7 @@ lcp_status pair_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const
   TC_TRY(make_map8(&mX, Xq, cin, tokens, N / 2, "mm8 X"));
   const int stage_bytes = M8_A + N * 64;
   const int raw = N * cdiv(cin, 128);
-  const int fixed = M8_SF * P8_SF_BYTES + P8_MAX_G + raw + 1024 + 512;
+  const int fixed = P8_SLOTS * P8_SLOT * P8_SF_BYTES + P8_MAX_G + raw + 1024 + 512;
   int stages = (227 * 1024 - fixed) / stage_bytes;
   if (stages > P8_MAX_STAGES) stages = P8_MAX_STAGES;
   const int smem = stages * stage_bytes + fixed;
