@@ -10,6 +10,8 @@
 // tokens the N side, whose width follows the token count; one lane is one
 // channel, so a warp's store of one token is 32 consecutive channels of Y.
 
+#include <algorithm>
+
 #include "tc_common.cuh"
 
 namespace lcp {
@@ -92,7 +94,8 @@ __device__ __forceinline__ bool elect_one() {
 // Waits of those two threads.  Their loops have no exit on a wait that gave up: a break there makes
 // the loop's values per-thread ones again (338 cycles against 206 for a wait, four products and a
 // commit).  Instead, once a wait of the CTA has given up, each later one returns at once, and the
-// loops run out over operands that are no longer meant to be right.
+// loops run out over operands that are no longer meant to be right.  The four groups of a whole
+// chunk are written out for the same reason (468 cycles a group in a loop, 200 written out).
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site) {
   if (!*abort_flag) mbar_wait_slow(bar, parity, abort_flag, site);
 }
@@ -112,7 +115,7 @@ constexpr int M8_BM = 128;            // output channels of a CTA: one row of we
 constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one scale group of channels)
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
 constexpr int M8_THREADS = 224;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6: scales
-constexpr int M8_MAX_STAGES = 8;
+constexpr int M8_MAX_STAGES = 12;
 constexpr int M8_SETS = 4;            // sets of scales in tensor memory
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
@@ -234,21 +237,24 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         const uint32_t sfa = tmem + (uint32_t)(NT + 8 * slot), sfb = sfa + 4;
         copy_scales(sfa, sdesc_scales(smem_u32(sf + slot * 1024)));
         copy_scales(sfb, sdesc_scales(smem_u32(sf + slot * 1024 + 512)));
-        const int jn = min(4, nk - 4 * c);
-        for (int j = 0; j < jn; ++j) {
+        auto group = [&](int j, int steps) {      // the products of group j of the chunk, 32 channels a step
           wait_through(full(stage), ph, abort_flag, 405);
           tc_fence_after();
           const uint64_t wd = wd0 + (uint32_t)(stage * (stage_bytes >> 4)), xd = xd0 + (uint32_t)(stage * (stage_bytes >> 4));
-          const int left = cin - (g0 + 4 * c + j) * 128;
           const uint32_t id = with_byte(idesc, j);
-          if (left >= 128) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_mx8(tmem, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
-          } else {                                           // C_in is a multiple of 32
-            for (int k = 0; k < left / 32; ++k) mma_mx8(tmem, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
-          }
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) mma_mx8(tmem, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
           mma_commit(empty(stage));
           if (++stage == stages) { stage = 0; ph ^= 1u; }
+        };
+        const int left = min(nk * 128, cin - g0 * 128) - 512 * c;      // channels from this chunk on
+        if (left >= 512) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) group(j, 4);
+        } else {                                                       // C_in is a multiple of 32
+#pragma unroll 1
+          for (int j = 0; 128 * j < left; ++j) group(j, min(4, (left - 128 * j) / 32));
         }
         mma_commit(sfempty(slot));
       }
@@ -450,6 +456,7 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         int mt, nt;
         tile_at(it, mt, nt);
         const int wrow = mt * 2 * M8_BM + (int)rank * M8_BM, xrow = nt * N + (int)rank * (N / 2);
+#pragma unroll 4
         for (int g = 0; g < G; ++g) {
           wait_through(empty(stage), ph ^ 1u, abort_flag, 411);
           issued |= 1u << stage;
@@ -492,21 +499,24 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
           copy_scales_pair(sfa, sdesc_scales(src));
           copy_scales_pair(sfb, sdesc_scales(src + 512));
           if (N > 128) copy_scales_pair(sfb + 4, sdesc_scales(src + 1024));
-          const int jn = min(4, G - 4 * c);
-          for (int j = 0; j < jn; ++j) {
+          auto group = [&](int j, int steps) {      // the products of group j of the chunk, 32 channels a step
             wait_through(full(stage), ph, abort_flag, 416);
             tc_fence_after();
             const uint64_t wd = wd0 + (uint32_t)(stage * (stage_bytes >> 4)), xd = xd0 + (uint32_t)(stage * (stage_bytes >> 4));
-            const int left = cin - (4 * c + j) * 128;
             const uint32_t id = with_byte(idesc, j);
-            if (left >= 128) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_mx8_pair(d, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
-            } else {
-              for (int k = 0; k < left / 32; ++k) mma_mx8_pair(d, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
-            }
+            for (int k = 0; k < 4; ++k)
+              if (k < steps) mma_mx8_pair(d, wd + 2 * k, xd + 2 * k, id, sfa, sfb, (c | j | k) != 0);
             mma_commit_pair(empty(stage), 0x3);
             if (++stage == stages) { stage = 0; ph ^= 1u; }
+          };
+          const int left = cin - 512 * c;
+          if (left >= 512) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) group(j, 4);
+          } else {
+#pragma unroll 1
+            for (int j = 0; 128 * j < left; ++j) group(j, min(4, (left - 128 * j) / 32));
           }
           mma_commit_pair(setfree(set), 0x1);
           if (++set == sets) { set = 0; sph ^= 1u; }
@@ -648,26 +658,42 @@ lcp_status make_map8(CUtensorMap* m, const void* base, int cin, int rows, int by
   return LCP_OK;
 }
 
+// How the split kernel cuts a product: tokens a tile, CTAs an SM, CTAs a tile (the C_in split).
+// Up to 32 tokens a ring stage is small and two CTAs share an SM, one's loads covering the other's
+// set-up and epilogue, unless there are so few CTAs that each can have a deep ring for itself.
+// The split is the largest that leaves every CTA three groups and all CTAs at once on the GPU:
+// 0.88 of the slots, since a GPC's SMs are not a multiple of every cluster size.  One token,
+// 4096 x 4096: 10.3 us without a split, 5.7 with 8; 4096 x 11008: 10.6 with 3 (258 CTAs), 14.5 with 4
+// (344, a second round); 13824 x 5120: 14.5 with 6 (240 CTAs), 20.6 with 7 (280).
+struct SplitPlan {
+  int NT, per_sm, S;
+  long long tiles;
+};
+SplitPlan split_plan(int cout, int cin, int tokens) {
+  SplitPlan p;
+  p.NT = tokens >= 128 ? 128 : (tokens + 15) / 16 * 16;
+  p.per_sm = p.NT <= 32 ? 2 : 1;
+  p.tiles = (long long)cdiv(cout, M8_BM) * cdiv(tokens, p.NT);
+  const int G = cdiv(cin, 128);
+  p.S = 8;
+  while (p.S > 1 && (p.S == 7 || 3 * p.S > G || 100 * p.tiles * p.S > 88LL * p.per_sm * num_sms())) --p.S;
+  if (p.tiles * p.S <= num_sms()) p.per_sm = 1;
+  return p;
+}
+
 template <typename OUT>
 lcp_status split_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, OUT* Y, int cout, int cin,
-                   int tokens, bool w_early, cudaStream_t st) {
-  const int NT = tokens >= 128 ? 128 : (tokens + 15) / 16 * 16;
+                   int tokens, const SplitPlan& p, bool w_early, cudaStream_t st) {
   CUtensorMap mW, mX;
   TC_TRY(make_map8(&mW, Wq, cin, cout, M8_BM, "mm8 W"));
-  TC_TRY(make_map8(&mX, Xq, cin, tokens, NT, "mm8 X"));
-  const long long tiles = (long long)cdiv(cout, M8_BM) * cdiv(tokens, NT);
-  const int G = cdiv(cin, 128);
-  // narrow tiles: two CTAs an SM, so that one's loads cover the other's set-up and epilogue
-  const int stage_bytes = M8_A + NT * 128;
-  const int per_sm = NT <= 32 ? 2 : 1;
-  int stages = (per_sm == 2 ? 104 * 1024 : 208 * 1024) / stage_bytes;
+  TC_TRY(make_map8(&mX, Xq, cin, tokens, p.NT, "mm8 X"));
+  const int stage_bytes = M8_A + p.NT * 128;
+  int stages = (p.per_sm == 2 ? 104 * 1024 : 218 * 1024) / stage_bytes;
   if (stages > M8_MAX_STAGES) stages = M8_MAX_STAGES;
-  int S = 1;
-  while (S < 8 && tiles * S * 2 <= (long long)per_sm * num_sms() && G >= 4 * S) S *= 2;
   const int smem = stages * stage_bytes + M8_SF * 1024 + 1024 + 512;
   TC_TRY(set_smem(mm8_split_kernel<OUT>, smem, "mm8"));
-  return launch_kernel(mm8_split_kernel<OUT>, dim3((unsigned)(tiles * S)), dim3(M8_THREADS), (size_t)smem, st, S, true,
-                       "mm8", mW, mX, Xs, Ws, Y, cout, cin, tokens, NT, stages, S, w_early ? 1 : 0);
+  return launch_kernel(mm8_split_kernel<OUT>, dim3((unsigned)(p.tiles * p.S)), dim3(M8_THREADS), (size_t)smem, st, p.S, true,
+                       "mm8", mW, mX, Xs, Ws, Y, cout, cin, tokens, p.NT, stages, p.S, w_early ? 1 : 0);
 }
 
 template <typename OUT>
@@ -690,15 +716,20 @@ lcp_status pair_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const
                        "mm8", mW, mX, Xs, Ws, Y, cout, cin, tokens, N, stages, raw, tokens <= cout ? 1 : 0);
 }
 
-// Tokens a tile of the pair kernel: the width whose rounds over the SM pairs cost least, a tile
-// costing its width and a fixed part (its fill and drain, and the W tile's share of the loads).
+// Tokens a tile of the pair kernel: the width whose rounds over the SM pairs cost least.  A round
+// costs, in nanoseconds, 95 + N a group (2048 x 4096 x 4096: 5.4 us a round of 32 groups at N = 64, 6.5
+// at 128, 11 at 240) but at least the 17 N that storing a tile takes, and some 600 to change tiles; the
+// last round's store shows (700 x 512 x 4096: 13.0 us with the 16 tokens a tile that the model without
+// the 600 picks, 8.1 with its 96).
 int pair_width(int cout, int cin, int tokens) {
+  const int G = cdiv(cin, 128), pairs = num_sms() / 2;
   int best = 16;
   long long cost = -1;
-  for (int N = 16; N <= P8_MAX_N && N * cdiv(cin, 128) <= P8_RAW; N += 16) {
+  for (int N = 16; N <= P8_MAX_N && N * G <= P8_RAW; N += 16) {
     const long long tiles = (long long)cdiv(cout, 2 * M8_BM) * cdiv(tokens, N);
-    const long long c = (tiles + num_sms() / 2 - 1) / (num_sms() / 2) * (N + 24);
-    if (cost < 0 || c <= cost) {
+    const long long round = std::max((long long)G * (95 + N), 17LL * N) + 600;
+    const long long c = (tiles + pairs - 1) / pairs * round + 11 * N;
+    if (cost < 0 || c < cost) {
       cost = c;
       best = N;
     }
@@ -706,12 +737,18 @@ int pair_width(int cout, int cin, int tokens) {
   return best;
 }
 
+// Above 128 tokens the pair kernel is ahead at every size measured (200 x 4096 x 4096: 10.9 us
+// against 12.2); between 65 and 128 it is where the split kernel has nothing to split, for want of
+// SMs or of channels (128 x 4096 x 11008: 15.0 against 17.8; 128 x 512 x 4096: 4.5 against 7.1; but
+// 128 x 11008 x 4096: 19.8 against 16.5).
 template <typename OUT>
 lcp_status mm8_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, OUT* Y, int cout, int cin,
                  int tokens, bool w_early, cudaStream_t st) {
-  if (tokens > 128 && cdiv(cin, 128) <= P8_MAX_G)
+  const SplitPlan p = split_plan(cout, cin, tokens);
+  const int G = cdiv(cin, 128);
+  if (G <= P8_MAX_G && (tokens > 128 || (tokens > 64 && (p.S == 1 || G <= 8))))
     return pair_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, pair_width(cout, cin, tokens), st);
-  return split_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, w_early, st);
+  return split_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, p, w_early, st);
 }
 
 }  // namespace
