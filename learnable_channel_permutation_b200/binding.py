@@ -619,15 +619,15 @@ def linear8(Wq: torch.Tensor, Ws: torch.Tensor, X: torch.Tensor, perm: Optional[
     Y = _shaped(Y, T, cout, out_dtype, X.device, "Y")
     if workspace is None:
         n = linear8_workspace(T, cin)
-        workspace = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=X.device)
+        workspace = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=X.device) if n else None
     _enqueue(lib().lcp_linear8, dev, w, ws, x, p, _arg(Y, Y.dtype, dev, "Y"), cout, cin, T, B, dt, _dt(Y),
-             _arg(workspace, torch.uint8, dev, "workspace"), workspace.numel())
+             _arg(workspace, torch.uint8, dev, "workspace"), 0 if workspace is None else workspace.numel())
     return Y
 
 
 @functools.lru_cache(maxsize=1024)
 def linear8_workspace(tokens: int, cin: int) -> int:
-    """Bytes of workspace linear8 needs."""
+    """Bytes of workspace linear8 needs (none up to 16 tokens)."""
     n = ctypes.c_size_t(0)
     check(lib().lcp_linear8_workspace_size(tokens, cin, ctypes.byref(n)))
     return int(n.value)

@@ -924,7 +924,7 @@ static size_t linear8_scales_at(int tokens, int cin) { return ((size_t)tokens * 
 lcp_status lcp_linear8_workspace_size(int tokens, int cin, size_t* bytes) {
   if (!bytes) return fail(LCP_ERR_NULL, "bytes is NULL");
   LCP_TRY(check_8bit(1, cin, nullptr, 0, tokens, {}));
-  *bytes = linear8_scales_at(tokens, cin) + (size_t)tokens * ((cin + 127) / 128);
+  *bytes = linear8_fused(tokens) ? 0 : linear8_scales_at(tokens, cin) + (size_t)tokens * ((cin + 127) / 128);
   return LCP_OK;
 }
 
@@ -938,10 +938,11 @@ lcp_status lcp_linear8(const uint8_t* Wq, const uint8_t* Ws, const void* X, cons
   if (tokens == 0) return LCP_OK;
   size_t need = 0;
   LCP_TRY(lcp_linear8_workspace_size(tokens, cin, &need));
-  if (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < need)
+  if (need && (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < need))
     return fail(LCP_ERR_WORKSPACE, "the workspace needs %zu bytes, 256-byte aligned", need);
   LCP_TRY(check_arch());
   LCP_TRY(check_pending());
+  if (linear8_fused(tokens)) return launch_linear8_fused(X, perm, B, Wq, Ws, Y, cout, cin, tokens, dtype, ydtype, stream);
   uint8_t* q = static_cast<uint8_t*>(ws);
   uint8_t* s = q + linear8_scales_at(tokens, cin);
   LCP_TRY(launch_quant8(X, perm, q, s, tokens, cin, B, dtype, stream));

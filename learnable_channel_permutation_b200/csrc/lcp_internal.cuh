@@ -312,6 +312,10 @@ lcp_status launch_quant8_weight(const void* W, const int32_t* perm, const uint32
                                 int cout, int cin, int B, lcp_dtype dt, cudaStream_t st);
 lcp_status launch_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, void* Y, int cout,
                       int cin, int tokens, lcp_dtype ydt, bool w_early, cudaStream_t st);
+// Few tokens: one launch that quantises X on the way (no workspace).
+bool linear8_fused(int tokens);
+lcp_status launch_linear8_fused(const void* X, const int32_t* perm, int B, const uint8_t* Wq, const uint8_t* Ws, void* Y,
+                                int cout, int cin, int tokens, lcp_dtype dt, lcp_dtype ydt, cudaStream_t st);
 lcp_status quant_error(int* site, int reset);
 lcp_status tc_error_mm8(int* site, int reset);
 

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 
+#include "quant8.cuh"
 #include "tc_common.cuh"
 
 namespace lcp {
@@ -114,7 +115,10 @@ __device__ __forceinline__ void wait_through_cluster(uint32_t bar, uint32_t pari
 constexpr int M8_BM = 128;            // output channels of a CTA: one row of weight scales
 constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one scale group of channels)
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
-constexpr int M8_THREADS = 224;       // warp 0: TMA, 1: MMA, 2-5: epilogue, 6: scales
+constexpr int M8_FUSED_TOKENS = 16;   // plain activations of up to so many tokens are quantised by the product itself
+constexpr int M8_FUSED_WARPS = 8;     // warps that do
+// warp 0: TMA, 1: MMA, 2-5: epilogue; 6: scales, or 2-9: quantisers
+template <typename XT> constexpr int m8_threads() { return sizeof(XT) == 1 ? 224 : 64 + 32 * M8_FUSED_WARPS; }
 constexpr int M8_MAX_STAGES = 12;
 constexpr int M8_SETS = 4;            // sets of scales in tensor memory
 
@@ -145,16 +149,26 @@ template <typename OUT> __device__ __forceinline__ void store4(OUT* out, const f
 // the instruction picks the byte of the group at hand.  Warp 6 builds the words of chunk c in
 // ring slot c % 4 once the products of chunk c - 4 are done, and the MMA thread copies them to
 // the tensor-memory set of the same number, which those products were the last to read.
-template <typename OUT>
-__global__ void __launch_bounds__(M8_THREADS)
+//
+// XT = uint8_t: X and Xs hold quantised activations; the tiles of X come by TMA, and warp 6
+// builds the scale words.  XT = float or bf16 (at most 16 tokens): X holds the activations
+// themselves, and eight warps quantise the CTA's channels (permuted, if PERM) straight into the
+// tiles and scale words.  Every CTA of a column of tiles quantises the same tokens again, 16 at
+// the most: that costs less than a launch that does it once (one token x 4096 x 4096: 8.0 us as
+// two launches).
+template <typename OUT, typename XT, bool PERM>
+__global__ void __launch_bounds__(m8_threads<XT>())
 mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                 const uint8_t* __restrict__ Xs, const uint8_t* __restrict__ Ws, OUT* __restrict__ Y, int cout, int cin,
-                 int tokens, int NT, int stages, int S, int w_early) {
+                 const XT* __restrict__ X, const int32_t* __restrict__ perm, int bmask, const uint8_t* __restrict__ Xs,
+                 const uint8_t* __restrict__ Ws, OUT* __restrict__ Y, int cout, int cin, int tokens, int NT, int stages,
+                 int S, int w_early) {
+  constexpr bool FUSED = sizeof(XT) != 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const int stage_bytes = M8_A + NT * 128;
   uint8_t* sf = smem + stages * stage_bytes;                  // M8_SF x (512 B of W, 512 B of X)
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sf + M8_SF * 1024);
+  uint32_t* exchange = reinterpret_cast<uint32_t*>(sf + M8_SF * 1024);   // PERM: a buffer for each quantising warp
+  uint64_t* bars = reinterpret_cast<uint64_t*>(exchange + (PERM ? M8_FUSED_WARPS * Q8_STAGE : 0));
   uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * M8_MAX_STAGES + 2 * M8_SF + 1);
   static_assert(M8_SETS == M8_SF, "a ring slot and a set are both free when the same products are done");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
@@ -170,7 +184,10 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const int tile = blockIdx.x / S;
   const int mt = tile % mtiles, nt = tile / mtiles;
   const int t0 = nt * NT;
-  const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);   // never empty: S <= G
+  // whole pairs of groups (a permutation's blocks are at most 256 channels); never empty: 3 S <= G
+  const int G2 = cdiv(G, 2);
+  const int g0 = 2 * (int)((long long)rank * G2 / S), g1 = min(G, 2 * (int)((long long)(rank + 1) * G2 / S));
+  const int npairs = (tokens + 1) / 2;     // FUSED: pairs of tokens, one for a warp or for several
   const int nk = g1 - g0, nchunk = cdiv(nk, 4);
 
   // accumulator columns [0, NT), then M8_SETS sets of (4 columns of W scales, 4 of X scales)
@@ -179,11 +196,11 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), FUSED ? 1 + npairs : 1);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < M8_SF; ++s) {
-      mbar_init(sffull(s), 32);
+      mbar_init(sffull(s), FUSED ? 2 * npairs : 32);
       mbar_init(sfempty(s), 1);
     }
     mbar_init(done, 1);
@@ -199,9 +216,10 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   if (warp == 0) {
     if (elect_one()) {
       uint32_t issued = 0, issued_par = 0;
+      const uint32_t bytes = FUSED ? M8_A : (uint32_t)stage_bytes;
       const int ahead = w_early ? min(stages, nk) : 0;
       for (int k = 0; k < ahead; ++k) {
-        mbar_expect_tx(full(k), (uint32_t)stage_bytes);
+        mbar_expect_tx(full(k), bytes);
         tma_load_2d(smem_u32(smem + k * stage_bytes), &tmW, full(k), (g0 + k) * 128, mt * M8_BM);
       }
       pdl_wait();
@@ -214,10 +232,10 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         issued_par = (issued_par & ~(1u << stage)) | (ph << stage);
         const uint32_t dst = smem_u32(smem + stage * stage_bytes);
         if (k >= ahead) {
-          mbar_expect_tx(full(stage), (uint32_t)stage_bytes);
+          mbar_expect_tx(full(stage), bytes);
           tma_load_2d(dst, &tmW, full(stage), (g0 + k) * 128, mt * M8_BM);
         }
-        tma_load_2d(dst + M8_A, &tmX, full(stage), (g0 + k) * 128, t0);
+        if (!FUSED) tma_load_2d(dst + M8_A, &tmX, full(stage), (g0 + k) * 128, t0);
         if (++stage == stages) { stage = 0; ph ^= 1u; }
       }
       for (int s = 0; s < stages; ++s)      // nothing of ours is in flight when the CTA ends
@@ -262,7 +280,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       mbar_wait_drain(done, 0, 406);
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (!FUSED && warp == 6) {
     pdl_wait();
     bool ok = true;
     for (int c = 0; c < nchunk && ok; ++c) {
@@ -293,6 +311,74 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       }
     }
   } else {
+    if constexpr (FUSED) {
+      // Warps 2-9: warp w takes the pair of tokens w % npp (npp: npairs rounded up to a power of two) and
+      // every `every`-th pair of groups, the next one's values loading meanwhile.  At most 8 / npp warps
+      // share a pair of tokens, and no more than stages / 2: a warp that waits for a tile knows from its
+      // own wait before, 2 every groups back, that the tile's use before the last is over, so the parity
+      // it waits for cannot be an older phase's.
+      pdl_wait();
+      const int w = warp - 2;
+      int npp = 1;
+      while (npp < npairs) npp *= 2;
+      const int pair = w % npp;
+      int every = M8_FUSED_WARPS / npp;
+      while (2 * every > stages) every /= 2;
+      uint32_t* buf = exchange + (PERM ? w * Q8_STAGE : 0);
+      const int row0 = 2 * pair;
+      auto load = [&](int p, int u) {
+        const int chan = (g0 + 2 * p) * 128 + 8 * lane;
+        return 2 * p < nk && chan < cin && row0 + u < tokens ? load8(X + (size_t)(row0 + u) * cin + chan) : zero8<XT>();
+      };
+      int p = pair < npairs && w / npp < every ? w / npp : 2 * nchunk;
+      Vec8<XT> next[2] = {load(p, 0), load(p, 1)};
+      for (; p < 2 * nchunk; p += every) {
+        Vec8<XT> v[2] = {next[0], next[1]};
+        next[0] = load(p + every, 0);
+        next[1] = load(p + every, 1);
+        const int c = p / 2, slot = c % M8_SF, chan = (g0 + 2 * p) * 128 + 8 * lane;
+        if (2 * p < nk) {
+          if (PERM) {
+            uint32_t to[8];
+            load_slots(perm, chan, cin, bmask, buf, to, &g_tc_error);
+            permute_rows(v[0], v[1], to, buf, lane);
+          }
+          uint32_t m[2];
+          group_max(v, m);
+          // the tile and slot are free once the products that read them last are done
+          const int k = 2 * p + (lane >> 4), s0 = 2 * p % stages, s1 = s0 + 1 == stages ? 0 : s0 + 1;
+          bool ok = mbar_wait(empty(s0), (uint32_t)(2 * p / stages + 1) & 1u, abort_flag, 409);
+          if (2 * p + 1 < nk) ok = mbar_wait(empty(s1), (uint32_t)((2 * p + 1) / stages + 1) & 1u, abort_flag, 409) && ok;
+          ok = mbar_wait(sfempty(slot), (uint32_t)(c / M8_SF + 1) & 1u, abort_flag, 410) && ok;
+          if (!warp_all(ok)) break;
+          uint8_t* words = sf + slot * 1024;
+          uint8_t* tile = smem + (lane < 16 ? s0 : s1) * stage_bytes + M8_A;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int row = row0 + u;
+            if (k >= nk || row >= tokens) break;
+            const uint32_t byte = scale_byte(m[u]);
+            *reinterpret_cast<uint2*>(tile + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4) + (lane & 1) * 8) =
+                to_e4m3(v[u], scale_inverse(byte));
+            if ((lane & 15) == 0) words[512 + row * 16 + 2 * (p & 1) + (lane >> 4)] = (uint8_t)byte;
+          }
+          if (pair == 0) {
+            const uint8_t* ws = Ws + (size_t)mt * G + g0 + 2 * p;
+            const uint32_t a = (uint32_t)__ldg(ws) | (2 * p + 1 < nk ? (uint32_t)__ldg(ws + 1) : 127u) << 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint16_t*>(words + lane * 16 + 4 * j + 2 * (p & 1)) = (uint16_t)a;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(full(s0));
+            if (2 * p + 1 < nk) mbar_arrive(full(s1));
+          }
+        }
+        if (lane == 0) mbar_arrive(sffull(slot));     // also for the missing half of the last chunk
+      }
+    }
+    if (warp < 6) {
     const int q = warp & 3;
     const int o = mt * M8_BM + q * 32 + lane;
     const bool ok = warp_all(mbar_wait(done, 0, abort_flag, 408));
@@ -311,6 +397,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         }
       }
     }
+    }
   }
   tc_fence_before();
   if (S > 1) {
@@ -320,7 +407,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int o = mt * M8_BM + 4 * lane;
     const int nmax = min(NT, tokens - t0);
 #pragma unroll 2
-    for (int n = rank + S * warp; n < nmax; n += S * (M8_THREADS / 32)) {
+    for (int n = rank + S * warp; n < nmax; n += S * (m8_threads<XT>() / 32)) {
       float4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -681,19 +768,22 @@ SplitPlan split_plan(int cout, int cin, int tokens) {
   return p;
 }
 
-template <typename OUT>
-lcp_status split_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, OUT* Y, int cout, int cin,
-                   int tokens, const SplitPlan& p, bool w_early, cudaStream_t st) {
+// XT = uint8_t: quantised activations X with scales Xs; otherwise the activations (Xs unused).
+template <typename OUT, typename XT, bool PERM>
+lcp_status split_t(const XT* X, const int32_t* perm, int B, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, OUT* Y,
+                   int cout, int cin, int tokens, const SplitPlan& p, bool w_early, cudaStream_t st) {
   CUtensorMap mW, mX;
   TC_TRY(make_map8(&mW, Wq, cin, cout, M8_BM, "mm8 W"));
-  TC_TRY(make_map8(&mX, Xq, cin, tokens, p.NT, "mm8 X"));
+  if (sizeof(XT) == 1) TC_TRY(make_map8(&mX, X, cin, tokens, p.NT, "mm8 X"));
+  else mX = mW;      // not used
   const int stage_bytes = M8_A + p.NT * 128;
-  int stages = (p.per_sm == 2 ? 104 * 1024 : 218 * 1024) / stage_bytes;
+  int stages = (p.per_sm == 2 ? 96 * 1024 : 210 * 1024) / stage_bytes;
   if (stages > M8_MAX_STAGES) stages = M8_MAX_STAGES;
-  const int smem = stages * stage_bytes + M8_SF * 1024 + 1024 + 512;
-  TC_TRY(set_smem(mm8_split_kernel<OUT>, smem, "mm8"));
-  return launch_kernel(mm8_split_kernel<OUT>, dim3((unsigned)(p.tiles * p.S)), dim3(M8_THREADS), (size_t)smem, st, p.S, true,
-                       "mm8", mW, mX, Xs, Ws, Y, cout, cin, tokens, p.NT, stages, p.S, w_early ? 1 : 0);
+  const int smem = stages * stage_bytes + M8_SF * 1024 + (PERM ? M8_FUSED_WARPS * Q8_STAGE * 4 : 0) + 1024 + 512;
+  const auto kernel = mm8_split_kernel<OUT, XT, PERM>;
+  TC_TRY(set_smem(kernel, smem, "mm8"));
+  return launch_kernel(kernel, dim3((unsigned)(p.tiles * p.S)), dim3(m8_threads<XT>()), (size_t)smem, st, p.S, true, "mm8",
+                       mW, mX, X, perm, B - 1, Xs, Ws, Y, cout, cin, tokens, p.NT, stages, p.S, w_early ? 1 : 0);
 }
 
 template <typename OUT>
@@ -748,7 +838,15 @@ lcp_status mm8_t(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const 
   const int G = cdiv(cin, 128);
   if (G <= P8_MAX_G && (tokens > 128 || (tokens > 64 && (p.S == 1 || G <= 8))))
     return pair_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, pair_width(cout, cin, tokens), st);
-  return split_t(Xq, Xs, Wq, Ws, Y, cout, cin, tokens, p, w_early, st);
+  return split_t<OUT, uint8_t, false>(Xq, nullptr, 1, Xs, Wq, Ws, Y, cout, cin, tokens, p, w_early, st);
+}
+
+template <typename OUT, typename XT>
+lcp_status fused_t(const XT* X, const int32_t* perm, int B, const uint8_t* Wq, const uint8_t* Ws, OUT* Y, int cout, int cin,
+                   int tokens, cudaStream_t st) {
+  const SplitPlan p = split_plan(cout, cin, tokens);
+  if (perm) return split_t<OUT, XT, true>(X, perm, B, nullptr, Wq, Ws, Y, cout, cin, tokens, p, false, st);
+  return split_t<OUT, XT, false>(X, perm, 1, nullptr, Wq, Ws, Y, cout, cin, tokens, p, false, st);
 }
 
 }  // namespace
@@ -759,6 +857,21 @@ lcp_status launch_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, c
                       int cin, int tokens, lcp_dtype ydt, bool w_early, cudaStream_t st) {
   if (ydt == LCP_F32) return mm8_t(Xq, Xs, Wq, Ws, static_cast<float*>(Y), cout, cin, tokens, w_early, st);
   return mm8_t(Xq, Xs, Wq, Ws, static_cast<__nv_bfloat16*>(Y), cout, cin, tokens, w_early, st);
+}
+
+bool linear8_fused(int tokens) { return tokens <= M8_FUSED_TOKENS; }
+
+lcp_status launch_linear8_fused(const void* X, const int32_t* perm, int B, const uint8_t* Wq, const uint8_t* Ws, void* Y,
+                                int cout, int cin, int tokens, lcp_dtype dt, lcp_dtype ydt, cudaStream_t st) {
+  const float* xf = static_cast<const float*>(X);
+  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(X);
+  float* yf = static_cast<float*>(Y);
+  __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(Y);
+  if (dt == LCP_F32)
+    return ydt == LCP_F32 ? fused_t(xf, perm, B, Wq, Ws, yf, cout, cin, tokens, st)
+                          : fused_t(xf, perm, B, Wq, Ws, yb, cout, cin, tokens, st);
+  return ydt == LCP_F32 ? fused_t(xb, perm, B, Wq, Ws, yf, cout, cin, tokens, st)
+                        : fused_t(xb, perm, B, Wq, Ws, yb, cout, cin, tokens, st);
 }
 
 }  // namespace lcp

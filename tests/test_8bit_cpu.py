@@ -91,15 +91,16 @@ def test_product_refusals():
     assert mm(Y=A + 8) == 7 and mm(Xq=A + 1) == 7
     assert mm(T=0) == 0
     n = ctypes.c_size_t(0)
-    assert L.lcp_linear8_workspace_size(5, 160, ctypes.byref(n)) == 0 and n.value >= 5 * 160 + 5 * 2
+    assert L.lcp_linear8_workspace_size(50, 160, ctypes.byref(n)) == 0 and n.value >= 50 * 160 + 50 * 2
+    assert L.lcp_linear8_workspace_size(16, 160, ctypes.byref(n)) == 0 and n.value == 0
     assert L.lcp_linear8_workspace_size(5, 161, ctypes.byref(n)) == 2
     assert L.lcp_linear8_workspace_size(5, 160, None) == 1
-    lin = lambda X=A, perm=None, Y=A, T=4, cin=128, B=0, dt=1, yt=0, ws=A, size=1 << 20: L.lcp_linear8(
+    lin = lambda X=A, perm=None, Y=A, T=40, cin=128, B=0, dt=1, yt=0, ws=A, size=1 << 20: L.lcp_linear8(
         A, A, X, perm, Y, 8, cin, T, B, dt, yt, ws, size, None)
     assert lin(X=None) == 1 and lin(Y=None) == 1
     assert lin(cin=80) == 2 and lin(perm=A, B=12) == 2
     assert lin(dt=5) == 3 and lin(yt=5) == 3
-    assert lin(ws=None) == 4 and lin(ws=A + 128) == 4 and lin(size=4 * 128 + 3) == 4
+    assert lin(ws=None) == 4 and lin(ws=A + 128) == 4 and lin(size=40 * 128 + 39) == 4
     assert lin(T=0, ws=None) == 0
 
 

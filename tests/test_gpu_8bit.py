@@ -267,6 +267,25 @@ def test_linear8_is_the_quantiser_and_the_product(gpu_lib, xdt, T, cin, cout, B)
     assert b.device_error() == 0
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 6, 9, 16])
+@pytest.mark.parametrize("cin,cout,B", [(4096, 11008, 64), (2272, 19200, 32), (13824, 640, 256)])
+def test_linear8_few_tokens_over_many_groups(gpu_lib, T, cin, cout, B):
+    """Ranges of channels several times the ring's length in one CTA, for every number of token pairs."""
+    rng = np.random.default_rng(T + cout)
+    X = _rows(rng, T, cin, "bf16").cuda()
+    perm = _dev_perm(_perm(rng, cin, B))
+    wq, ws = (t.cuda() for t in _operand(rng, cout, cin, -(-cout // 128)))
+    Y = b.linear8(wq, ws, X, perm)
+    q, s = b.quant8(X, perm)
+    assert torch.equal(Y, b.mm8(q, s, wq, ws))
+    assert b.device_error() == 0
+    rows = np.unique(np.concatenate([np.arange(0, cout, 37), [cout - 1]]))
+    sel = torch.from_numpy(rows).cuda()
+    w = _np(wq.view(torch.uint8)[sel].view(b.E4M3)) * np.repeat(_np(ws), 128, 1)[rows // 128][:, :cin]
+    x = O.dequant8(_np(q), _np(s), 1)
+    assert np.all(np.abs(_np(Y)[:, rows] - x @ w.T) <= (cin / 32 + 40) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T))
+
+
 def test_no_tokens(gpu_lib):
     wq, ws = (t.cuda() for t in _operand(np.random.default_rng(0), 40, 128, 1))
     X = torch.empty(0, 128, device="cuda")
