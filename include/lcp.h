@@ -457,7 +457,7 @@ LCP_API lcp_status lcp_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* 
 
 /* ("Effect on inference acceleration": the permuted layer at run time) lcp_quant8 of X and lcp_mm8 with the result: the
  * 8-bit layer on activations X [T, C_in] in `dtype`, original channel order when perm is given.  ws: a device buffer of at
- * least lcp_linear8_workspace_size() bytes, 256-byte aligned, not used by an overlapping call; up to 16 tokens need none
+ * least lcp_linear8_workspace_size() bytes, 256-byte aligned, not used by an overlapping call; up to 8 tokens need none
  * (size 0, ws may be NULL): one kernel then quantises X as it multiplies. */
 LCP_API lcp_status lcp_linear8_workspace_size(int tokens, int cin, size_t* bytes);
 LCP_API lcp_status lcp_linear8(const uint8_t* Wq, const uint8_t* Ws, const void* X, const int32_t* perm, void* Y,

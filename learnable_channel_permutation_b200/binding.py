@@ -627,7 +627,7 @@ def linear8(Wq: torch.Tensor, Ws: torch.Tensor, X: torch.Tensor, perm: Optional[
 
 @functools.lru_cache(maxsize=1024)
 def linear8_workspace(tokens: int, cin: int) -> int:
-    """Bytes of workspace linear8 needs (none up to 16 tokens)."""
+    """Bytes of workspace linear8 needs (none up to 8 tokens)."""
     n = ctypes.c_size_t(0)
     check(lib().lcp_linear8_workspace_size(tokens, cin, ctypes.byref(n)))
     return int(n.value)

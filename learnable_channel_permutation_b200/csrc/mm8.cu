@@ -115,9 +115,10 @@ __device__ __forceinline__ void wait_through_cluster(uint32_t bar, uint32_t pari
 constexpr int M8_BM = 128;            // output channels of a CTA: one row of weight scales
 constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one scale group of channels)
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
-constexpr int M8_FUSED_TOKENS = 16;   // plain activations of up to so many tokens are quantised by the product itself
-constexpr int M8_FUSED_WARPS = 8;     // warps that do
-// warp 0: TMA, 1: MMA, 2-5: epilogue; 6: scales, or 2-9: quantisers
+constexpr int M8_FUSED_TOKENS = 8;    // plain activations of up to so many tokens are quantised by the product itself
+                                      // (16 tokens x 4096 x 11008: 18.2 us, 13.2 as two launches; 8 tokens: 12.5)
+constexpr int M8_FUSED_WARPS = 8;     // warps that do (16 leave one CTA an SM: 16.2 us instead of 6.9 at 4096 x 4096)
+// warp 0: TMA, 1: MMA, 2-5: epilogue; 6: scales, or all from 2 on: quantisers
 template <typename XT> constexpr int m8_threads() { return sizeof(XT) == 1 ? 224 : 64 + 32 * M8_FUSED_WARPS; }
 constexpr int M8_MAX_STAGES = 12;
 constexpr int M8_SETS = 4;            // sets of scales in tensor memory
@@ -151,9 +152,9 @@ template <typename OUT> __device__ __forceinline__ void store4(OUT* out, const f
 // the tensor-memory set of the same number, which those products were the last to read.
 //
 // XT = uint8_t: X and Xs hold quantised activations; the tiles of X come by TMA, and warp 6
-// builds the scale words.  XT = float or bf16 (at most 16 tokens): X holds the activations
+// builds the scale words.  XT = float or bf16 (at most 8 tokens): X holds the activations
 // themselves, and eight warps quantise the CTA's channels (permuted, if PERM) straight into the
-// tiles and scale words.  Every CTA of a column of tiles quantises the same tokens again, 16 at
+// tiles and scale words.  Every CTA of a column of tiles quantises the same tokens again, 8 at
 // the most: that costs less than a launch that does it once (one token x 4096 x 4096: 8.0 us as
 // two launches).
 template <typename OUT, typename XT, bool PERM>
@@ -312,8 +313,8 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
   } else {
     if constexpr (FUSED) {
-      // Warps 2-9: warp w takes the pair of tokens w % npp (npp: npairs rounded up to a power of two) and
-      // every `every`-th pair of groups, the next one's values loading meanwhile.  At most 8 / npp warps
+      // Warps from 2 on: warp w takes the pair of tokens w % npp (npp: npairs rounded up to a power of two) and
+      // every `every`-th pair of groups, the next one's values loading meanwhile.  At most M8_FUSED_WARPS / npp warps
       // share a pair of tokens, and no more than stages / 2: a warp that waits for a tile knows from its
       // own wait before, 2 every groups back, that the tile's use before the last is over, so the parity
       // it waits for cannot be an older phase's.

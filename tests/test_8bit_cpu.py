@@ -92,7 +92,7 @@ def test_product_refusals():
     assert mm(T=0) == 0
     n = ctypes.c_size_t(0)
     assert L.lcp_linear8_workspace_size(50, 160, ctypes.byref(n)) == 0 and n.value >= 50 * 160 + 50 * 2
-    assert L.lcp_linear8_workspace_size(16, 160, ctypes.byref(n)) == 0 and n.value == 0
+    assert L.lcp_linear8_workspace_size(8, 160, ctypes.byref(n)) == 0 and n.value == 0
     assert L.lcp_linear8_workspace_size(5, 161, ctypes.byref(n)) == 2
     assert L.lcp_linear8_workspace_size(5, 160, None) == 1
     lin = lambda X=A, perm=None, Y=A, T=40, cin=128, B=0, dt=1, yt=0, ws=A, size=1 << 20: L.lcp_linear8(
