@@ -309,9 +309,10 @@ class _TensorList:
         self.ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8, device=device)
         self.norm_out = torch.empty(1, dtype=torch.float32, device=device)
         self.tail = (self.norm_out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        self.head = (ctypes.cast(self.arr, ctypes.POINTER(self.arr._type_)), count)
 
     def _call(self, fn, *args, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-        _enqueue(fn, self.device.index, self.arr, self.n, *args, *self.tail, stream=stream)
+        _enqueue(fn, self.device.index, *self.head, *args, *self.tail, stream=stream)
         return self.norm_out
 
 
@@ -542,13 +543,14 @@ def _groups(n: int) -> int:
     return (n + GROUP8 - 1) // GROUP8
 
 
-def _shaped(t: Optional[torch.Tensor], rows: int, cols: int, dtype, device, name: str) -> torch.Tensor:
-    """``t``, or a new [rows, cols] tensor when it is None."""
+def _output(t: Optional[torch.Tensor], rows: int, cols: int, dtype, X: torch.Tensor, index: int, name: str):
+    """``t`` and its address, or a new [rows, cols] tensor on X's device when it is None."""
     if t is None:
-        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+        t = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=X.device)
+        return t, t.data_ptr()
     if t.shape != (rows, cols):
         raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
-    return t
+    return t, _arg(t, dtype, index, name)
 
 
 def quant8(X: torch.Tensor, perm: Optional[torch.Tensor] = None, Q: Optional[torch.Tensor] = None,
@@ -558,9 +560,9 @@ def quant8(X: torch.Tensor, perm: Optional[torch.Tensor] = None, Q: Optional[tor
     T, cin = X.shape
     B, dev, dt = _perm8(perm, cin), X.get_device(), _dt(X)
     x, p = _arg(X, X.dtype, dev, "X"), _arg(perm, torch.int32, dev, "perm")
-    Q = _shaped(Q, T, cin, E4M3, X.device, "Q")
-    S = _shaped(S, T, _groups(cin), E8M0, X.device, "S")
-    _enqueue(lib().lcp_quant8, dev, x, p, _arg(Q, E4M3, dev, "Q"), _arg(S, E8M0, dev, "S"), T, cin, B, dt)
+    Q, q = _output(Q, T, cin, E4M3, X, dev, "Q")
+    S, s = _output(S, T, _groups(cin), E8M0, X, dev, "S")
+    _enqueue(lib().lcp_quant8, dev, x, p, q, s, T, cin, B, dt)
     return Q, S
 
 
@@ -575,9 +577,9 @@ def quant8_weight(W: torch.Tensor, perm: Optional[torch.Tensor] = None, mask_bit
     if mask_bits is not None and mask_bits.numel() * 32 != cout * cin:
         raise ValueError("mask_bits must be [C_out, C_in/32]")
     bits = _arg(mask_bits, torch.int32, dev, "mask_bits")
-    Q = _shaped(Q, cout, cin, E4M3, W.device, "Q")
-    S = _shaped(S, _groups(cout), _groups(cin), E8M0, W.device, "S")
-    _enqueue(lib().lcp_quant8_weight, dev, w, p, bits, _arg(Q, E4M3, dev, "Q"), _arg(S, E8M0, dev, "S"), cout, cin, B, dt)
+    Q, q = _output(Q, cout, cin, E4M3, W, dev, "Q")
+    S, s = _output(S, _groups(cout), _groups(cin), E8M0, W, dev, "S")
+    _enqueue(lib().lcp_quant8_weight, dev, w, p, bits, q, s, cout, cin, B, dt)
     return Q, S
 
 
@@ -601,8 +603,8 @@ def mm8(Xq: torch.Tensor, Xs: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, 
     if Xs.shape != (T, _groups(cin)):
         raise ValueError(f"Xs must be [T, ceil(C_in/128)], got {tuple(Xs.shape)}")
     cout, w, ws = _weight8(Wq, Ws, cin, dev)
-    Y = _shaped(Y, T, cout, out_dtype, Xq.device, "Y")
-    _enqueue(lib().lcp_mm8, dev, x, _arg(Xs, E8M0, dev, "Xs"), w, ws, _arg(Y, Y.dtype, dev, "Y"), cout, cin, T, _dt(Y))
+    Y, y = _output(Y, T, cout, out_dtype if Y is None else Y.dtype, Xq, dev, "Y")
+    _enqueue(lib().lcp_mm8, dev, x, _arg(Xs, E8M0, dev, "Xs"), w, ws, y, cout, cin, T, _dt(Y))
     return Y
 
 
@@ -616,11 +618,11 @@ def linear8(Wq: torch.Tensor, Ws: torch.Tensor, X: torch.Tensor, perm: Optional[
     B, dev, dt = _perm8(perm, cin), X.get_device(), _dt(X)
     x, p = _arg(X, X.dtype, dev, "X"), _arg(perm, torch.int32, dev, "perm")
     cout, w, ws = _weight8(Wq, Ws, cin, dev)
-    Y = _shaped(Y, T, cout, out_dtype, X.device, "Y")
+    Y, y = _output(Y, T, cout, out_dtype if Y is None else Y.dtype, X, dev, "Y")
     if workspace is None:
         n = linear8_workspace(T, cin)
         workspace = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=X.device) if n else None
-    _enqueue(lib().lcp_linear8, dev, w, ws, x, p, _arg(Y, Y.dtype, dev, "Y"), cout, cin, T, B, dt, _dt(Y),
+    _enqueue(lib().lcp_linear8, dev, w, ws, x, p, y, cout, cin, T, B, dt, _dt(Y),
              _arg(workspace, torch.uint8, dev, "workspace"), 0 if workspace is None else workspace.numel())
     return Y
 

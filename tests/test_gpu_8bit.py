@@ -201,6 +201,12 @@ def test_mm8_many_tiles(gpu_lib, T):
     _check(*_product(np.random.default_rng(T), T, 1024, 11008, torch.bfloat16))
 
 
+@pytest.mark.parametrize("T,cin,cout", [(150, 33024, 136), (20, 40000, 72), (5000, 96, 8), (3, 32, 19000), (1, 32768 * 4, 130)])
+def test_mm8_long_and_narrow(gpu_lib, T, cin, cout):
+    """More channels than a tile's scales are staged for, many tokens of few channels, many outputs of one group."""
+    _check(*_product(np.random.default_rng(T + cin), T, cin, cout))
+
+
 def test_mm8_scales_of_every_row_and_group(gpu_lib):
     """One nonzero value a row at a time, with scales that name the row and the group."""
     T, cin, cout = 300, 1408, 400

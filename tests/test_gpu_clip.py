@@ -80,6 +80,30 @@ def test_outputs_stay_inside_their_tensors(gpu_lib):
     assert torch.all(flat[5:10002] < 1.0) and torch.all(flat[10007:20000] < 1.0)
 
 
+@pytest.mark.parametrize("sizes", [[70], [65536], [65537], [64 * 64 * 64], [700001], [4096] * 16, [4097] * 16, [9] * 17,
+                                   [100] * 80, [100] * 81, [30011] * 90])
+def test_every_way_a_list_is_cut(gpu_lib, sizes):
+    """Both sides of each border between the launches' forms, in place, with a workspace full of garbage."""
+    ts = _tensors(sizes, sum(sizes))
+    ref = _f64(ts)
+    norm = O.grad_norm(ref)
+    lst = b.GradList(ts)
+    lst.ws.fill_(0xff)
+    assert abs(float(lst.norm()) - norm) <= NORM_TOL * norm
+    lst.ws.fill_(0xff)
+    assert abs(float(lst.clip(0.5 * norm)) - norm) <= NORM_TOL * norm
+    f = O.clip_factor(norm, 0.5 * norm)
+    for t, r in zip(ts, ref):
+        assert np.all(np.abs(t.double().cpu().numpy() - r * f) <= 2.0 ** -22 * np.abs(r * f))
+    L, g, m, v = _adam_state(sizes, 2, 4)
+    Lr = [O.adamw_update(*[x[i].double().cpu().numpy() for x in (L, g, m, v)], 4, lr=1e-3) for i in range(len(sizes))]
+    before = [x.double().cpu().numpy() for x in L]
+    b.AdamwList(L, g, m, v).run(b.adamw_params(lr=1e-3), 4)
+    for i in range(len(sizes)):
+        assert H.relerr(m[i].cpu().numpy(), Lr[i][1]) <= 1e-6 and H.relerr(v[i].cpu().numpy(), Lr[i][2]) <= 1e-6
+        assert H.relerr(L[i].double().cpu().numpy() - before[i], Lr[i][0] - before[i]) <= 1e-4
+
+
 def test_more_tensors_than_one_launch_takes(gpu_lib):
     ts = _tensors([17 + i % 9 for i in range(1500)], 8)
     norm = O.grad_norm(_f64(ts))
