@@ -7,6 +7,7 @@
 //   evaluated as (M.W' P_B^T) X  ->  token-mean cosine loss (objective)
 //   ->  reverse pass to the logits with the mask held constant.
 
+#include <atomic>
 #include <cstdlib>
 #include <cmath>
 #include <cstdarg>
@@ -54,6 +55,23 @@ lcp_status ensure_smem_limit(const void* func, int bytes, const char* what) {
   }
   if (nseen < 256) seen[nseen++] = Entry{func, dev, bytes};
   return LCP_OK;
+}
+
+int device_sms() {
+  static std::atomic<int> known[64];      // 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 148;
+  }
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 bool pdl_enabled() {

@@ -311,12 +311,6 @@ small_kernel(const __grid_constant__ Table t, double max_norm, float* __restrict
   cluster.barrier_wait();        // no CTA ends while another may still read its sum
 }
 
-int sm_count() {
-  int sms = 148, dev = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
 long long chunks_of(long long n, int chunk) { return (n + chunk - 1) / chunk; }
 // Short chunks where long ones would leave SMs without any (one layer's logits, 128 chunks instead of 32:
 // 4.5 us instead of 6.2 clipped, 5.5 instead of 9.3 updated; but seven layers', 962 instead of 241: 8.8
@@ -499,7 +493,7 @@ lcp_status run_list(const Desc* d, int count, double max_norm, float* norm, void
     const int chunks = fill(t, d, count, kSmallChunk, &at);
     return run_small<APPLY, T>(t, chunks, max_norm, norm, c, st, what);
   }
-  const int sms = sm_count();
+  const int sms = device_sms();
   double* partials = static_cast<double*>(ws);
   if (use_short_chunks(d, count, sms))
     return run_passes<APPLY, kShortChunk, T>(t, d, count, max_norm, norm, partials, c, sms, st, what);
@@ -511,7 +505,7 @@ lcp_status run_list(const Desc* d, int count, double max_norm, float* norm, void
 size_t clip_workspace(int count) {
   // one partial for each CTA of each launch
   const size_t launches = (size_t)count / kCapLarge + 1;
-  return launches * (size_t)kClipCtasPerSm * sm_count() * sizeof(double);
+  return launches * (size_t)kClipCtasPerSm * device_sms() * sizeof(double);
 }
 
 lcp_status launch_grad_norm(const lcp_grad* d, int count, float* norm, void* ws, cudaStream_t st) {

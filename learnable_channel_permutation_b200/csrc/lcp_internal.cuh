@@ -23,6 +23,9 @@ lcp_status check_pending();
 // unless an earlier call already did (the attribute persists for the process).
 lcp_status ensure_smem_limit(const void* func, int bytes, const char* what);
 
+// SMs of the current device (148 where there is none to ask), asked once a device.
+int device_sms();
+
 // ---- programmatic dependent launch -------------------------------------
 // A kernel launched with pdl = true (launch_kernel below) may start while the
 // kernel before it on the stream is still finishing.  It calls pdl_wait()

@@ -341,7 +341,7 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         if (2 * p < nk) {
           if (PERM) {
             uint32_t to[8];
-            load_slots(perm, chan, cin, bmask, buf, to, &g_tc_error);
+            load_slots(perm, chan, lane, cin, bmask, buf, to, &g_tc_error);
             permute_rows(v[0], v[1], to, buf, lane);
           }
           uint32_t m[2];

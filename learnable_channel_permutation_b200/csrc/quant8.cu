@@ -27,8 +27,6 @@ namespace {
 __device__ int g_quant_error;   // first invalid permutation entry seen (302), 0 if none
 
 constexpr int Q8_ROW_WARPS = 8;    // activations: warps per CTA
-constexpr int Q8_W_WARPS = 16;     // weights: warps per CTA
-constexpr int Q8_W_ROWS = 128 / Q8_W_WARPS;   // weight rows of a warp
 
 // Zeroes the values whose bit of `keep` (eight bits) is clear.  bf16: a product spreads four bits
 // to the top bits of four bytes, whose signs a byte permutation then copies over a pair of values.
@@ -75,7 +73,7 @@ quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, ui
   int t = blockIdx.y * Q8_ROW_WARPS + warp;
   Vec8<T> next[2] = {load(t), load(t + step)};
   uint32_t slot[8];
-  if (PERM) load_slots(perm, chan, cin, bmask, stage[warp], slot, &g_quant_error);
+  if (PERM) load_slots(perm, chan, lane, cin, bmask, stage[warp], slot, &g_quant_error);
   for (; t < tokens; t += 2 * step) {
     Vec8<T> v[2] = {next[0], next[1]};
     next[0] = load(t + 2 * step);
@@ -94,35 +92,55 @@ quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, ui
   }
 }
 
-// Weights.  A CTA takes 128 rows x 256 channels (two blocks), eight rows a warp,
-// and holds the values in registers (in their stored type) while the two block
-// maxima are reduced.
-template <typename T, bool PERM, bool MASK>
-__global__ void __launch_bounds__(32 * Q8_W_WARPS, sizeof(T) == 2 ? 2 : 1)
+// Weights.  A CTA takes 128 rows x CH channels and holds the values in registers (in their stored
+// type, 32 registers a lane) while the block maxima are reduced.  CH = 256 (two blocks, a warp to a
+// row) for B = 256 and for every permuted bf16 weight, 128 (half a warp to a row) otherwise:
+// smaller CTAs overlap their phases better (5120 x 13824 as it is: 32.2 us, 33.7 at CH = 256; float32
+// permuted: 90 us, 104), but bf16's exchange does not gain by it (permuted and masked: 49.7 us at
+// CH = 128, 47.3 at 256).
+template <typename T> constexpr int w_loads() { return 16 / (int)sizeof(T); }     // of a lane, each eight channels of a row
+template <typename T, int CH> constexpr int w_warps() { return CH / 2 / w_loads<T>(); }
+template <typename T, bool PERM, bool MASK, int CH>
+__global__ void __launch_bounds__(32 * w_warps<T, CH>(), 32 / w_warps<T, CH>())
 quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, const uint8_t* __restrict__ mask,
                      uint8_t* __restrict__ Q, uint8_t* __restrict__ S, int cout, int cin, int bmask) {
-  __shared__ __align__(16) uint32_t stage[PERM ? Q8_W_WARPS : 1][PERM ? Q8_STAGE : 4];
-  __shared__ uint32_t part[Q8_W_WARPS][2];
+  constexpr int LOADS = w_loads<T>(), WARPS = w_warps<T, CH>();
+  constexpr int ROWS = 256 / CH;     // of a warp's load
+  __shared__ __align__(16) uint32_t stage[PERM ? WARPS : 1][PERM ? Q8_STAGE : 4];
+  __shared__ uint32_t part[WARPS][2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
+  const int chan = blockIdx.x * CH + 8 * (lane & (CH / 8 - 1));
   const int G = (cin + 127) / 128;
   const bool in = chan < cin;
+  const int o0 = blockIdx.y * 128 + warp * ROWS + (CH == 128 ? lane >> 4 : 0);
   pdl_wait();
   pdl_trigger();
-  Vec8<T> v[Q8_W_ROWS];
+  Vec8<T> v[LOADS];
   uint32_t keep[2] = {0u, 0u};      // a row's eight mask bits in a byte
+  // rows and channels of a whole tile are loaded and stored without bounds checks
+  const bool whole = (int)(blockIdx.y + 1) * 128 <= cout && (int)(blockIdx.x + 1) * CH <= cin;
+  const size_t step = (size_t)(WARPS * ROWS) * cin;
+  const T* w0 = W + (size_t)o0 * cin + chan;
+  const uint8_t* m0 = MASK ? mask + (size_t)o0 * (cin / 8) + chan / 8 : nullptr;
+  if (whole) {
 #pragma unroll
-  for (int r = 0; r < Q8_W_ROWS; ++r) {
-    const int o = blockIdx.y * 128 + r * Q8_W_WARPS + warp;
-    const bool ok = in && o < cout;
-    v[r] = ok ? load8(W + (size_t)o * cin + chan) : zero8<T>();
-    if (MASK && ok) keep[r / 4] |= (uint32_t)__ldg(mask + (size_t)o * (cin / 8) + chan / 8) << (8 * (r % 4));
+    for (int r = 0; r < LOADS; ++r) {
+      v[r] = load8(w0 + r * step);
+      if (MASK) keep[r / 4] |= (uint32_t)__ldg(m0 + r * (step / 8)) << (8 * (r % 4));
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < LOADS; ++r) {
+      const bool ok = in && o0 + r * WARPS * ROWS < cout;
+      v[r] = ok ? load8(w0 + r * step) : zero8<T>();
+      if (MASK && ok) keep[r / 4] |= (uint32_t)__ldg(m0 + r * (step / 8)) << (8 * (r % 4));
+    }
   }
   uint32_t slot[8];
-  if (PERM) load_slots(perm, chan, cin, bmask, stage[warp], slot, &g_quant_error);
+  if (PERM) load_slots(perm, chan, lane, cin, bmask, stage[warp], slot, &g_quant_error);
   uint32_t m = 0;
 #pragma unroll
-  for (int r = 0; r < Q8_W_ROWS; ++r) {
+  for (int r = 0; r < LOADS; ++r) {
     if (PERM && r % 2 == 0) permute_rows(v[r], v[r + 1], slot, stage[warp], lane);
     if (MASK) apply_mask(v[r], keep[r / 4] >> (8 * (r % 4)));
     m = max(m, amax8(v[r]));
@@ -132,27 +150,22 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
   __syncthreads();
   m = 0;
 #pragma unroll
-  for (int w = 0; w < Q8_W_WARPS; ++w) m = max(m, part[w][lane >> 4]);
+  for (int w = 0; w < WARPS; ++w) m = max(m, CH == 128 ? max(part[w][0], part[w][1]) : part[w][lane >> 4]);
   const uint32_t byte = scale_byte(m);
   const float inv = scale_inverse(byte);
   if (!in) return;
+  uint8_t* q0 = Q + (size_t)o0 * cin + chan;
 #pragma unroll
-  for (int r = 0; r < Q8_W_ROWS; ++r) {
-    const int o = blockIdx.y * 128 + r * Q8_W_WARPS + warp;
-    if (o >= cout) break;
-    *reinterpret_cast<uint2*>(Q + (size_t)o * cin + chan) = to_e4m3(v[r], inv);
-  }
-  if (warp == 0 && (lane & 15) == 0) S[(size_t)blockIdx.y * G + chan / 128] = (uint8_t)byte;
+  for (int r = 0; r < LOADS; ++r)
+    if (whole || o0 + r * WARPS * ROWS < cout) *reinterpret_cast<uint2*>(q0 + r * step) = to_e4m3(v[r], inv);
+  if (warp == 0 && (lane == 0 || (CH == 256 && lane == 16))) S[(size_t)blockIdx.y * G + chan / 128] = (uint8_t)byte;
 }
 
 int cdiv_host(int a, int b) { return (a + b - 1) / b; }
 
 template <typename T>
 lcp_status rows_t(const T* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B, cudaStream_t st) {
-  int sms = 148, dev = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int chunks = cdiv_host(cin, Q8_CHUNK);
+  const int sms = device_sms(), chunks = cdiv_host(cin, Q8_CHUNK);
   // as many CTAs as fit the GPU at once (one more would cost a second round of all of them)
   const int fit = (perm ? row_ctas<T, true>() : row_ctas<T, false>()) * sms / chunks;
   const int gy = std::min(cdiv_host(tokens, Q8_ROW_WARPS), std::max(fit, 1));
@@ -165,17 +178,22 @@ lcp_status rows_t(const T* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int t
                        tokens, cin, bmask);
 }
 
+template <typename T, bool PERM, int CH>
+lcp_status weight_ch(const T* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S, int cout, int cin,
+                     int B, cudaStream_t st) {
+  const dim3 grid((unsigned)cdiv_host(cin, CH), (unsigned)cdiv_host(cout, 128)), block(32 * w_warps<T, CH>());
+  const uint8_t* mb = reinterpret_cast<const uint8_t*>(mask);
+  const auto kernel = mask ? quant8_weight_kernel<T, PERM, true, CH> : quant8_weight_kernel<T, PERM, false, CH>;
+  return launch_kernel(kernel, grid, block, 0, st, 1, true, "quant8_weight", W, perm, mb, Q, S, cout, cin, B - 1);
+}
 template <typename T>
 lcp_status weight_t(const T* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S, int cout, int cin,
                     int B, cudaStream_t st) {
-  const dim3 grid((unsigned)cdiv_host(cin, Q8_CHUNK), (unsigned)cdiv_host(cout, 128)), block(32 * Q8_W_WARPS);
-  const uint8_t* mb = reinterpret_cast<const uint8_t*>(mask);
-  const int bmask = perm ? B - 1 : 0;
-  auto go = [&](auto kernel) {
-    return launch_kernel(kernel, grid, block, 0, st, 1, true, "quant8_weight", W, perm, mb, Q, S, cout, cin, bmask);
-  };
-  if (perm) return mask ? go(quant8_weight_kernel<T, true, true>) : go(quant8_weight_kernel<T, true, false>);
-  return mask ? go(quant8_weight_kernel<T, false, true>) : go(quant8_weight_kernel<T, false, false>);
+  if (!perm) return weight_ch<T, false, 128>(W, perm, mask, Q, S, cout, cin, 1, st);
+  if constexpr (sizeof(T) == 4) {
+    if (B != 256) return weight_ch<T, true, 128>(W, perm, mask, Q, S, cout, cin, B, st);
+  }
+  return weight_ch<T, true, 256>(W, perm, mask, Q, S, cout, cin, B, st);
 }
 
 }  // namespace

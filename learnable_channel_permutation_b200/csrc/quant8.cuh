@@ -52,7 +52,7 @@ constexpr int Q8_STAGE = Q8_CHUNK + 4;   // words of a warp's exchange buffer; w
 // addresses): word 256 for a permutation entry outside [0, B); their own places past the last
 // channel (their zeros are moved like values, so that every slot is written).  A bad entry is
 // recorded in *error.
-__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int cin, int bmask,
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int lane, int cin, int bmask,
                                            const uint32_t* buf, uint32_t (&slot)[8], int* error) {
   int4 p[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
   if (chan < cin) {
@@ -64,7 +64,7 @@ __device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int own = (chan + j) & (Q8_CHUNK - 1);
+    const int own = 8 * lane + j;
     const bool out = (unsigned)e[j] > (unsigned)bmask;
     bad |= out;
     slot[j] = base + 4u * (uint32_t)(chan >= cin ? own : (out ? Q8_CHUNK : (own & ~bmask) | e[j]));
