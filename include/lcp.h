@@ -231,6 +231,8 @@ LCP_API lcp_status lcp_train(const lcp_layer* layers, int nlayers, const lcp_hpa
  *   f = min(1, max_norm / (norm + 1e-6)).
  * A norm that is not finite is passed on: NaN makes the factor NaN, infinity
  * makes it 0 (a gradient that is itself infinite or NaN then becomes NaN).
+ * With an infinite max_norm f is 1 whatever the norm: nothing is clipped, and
+ * a gradient that is not finite reaches its own value alone.
  * Tensors of one list must not overlap each other (not checked here; the
  * Python lists check it).  Any length from 0 on and any alignment to the
  * element type are taken; 16-byte aligned tensors run fastest.  `ws` is a

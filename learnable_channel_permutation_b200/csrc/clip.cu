@@ -8,7 +8,7 @@
 //   AdamW with f g as the gradient (adamw; the formulas of adamw.cu)
 //
 // A norm that is not finite is passed on: NaN makes every clipped gradient NaN,
-// infinity makes f zero.
+// infinity makes f zero.  max_norm infinite: f = 1, whatever the norm.
 //
 // Bound by HBM (three float32 operations a value).  The squares and their sums
 // are float64: no gradient overflows or underflows in them, and the sum of a
@@ -168,7 +168,7 @@ __device__ __forceinline__ double norm_of(const double* __restrict__ partials, i
 }
 __device__ __forceinline__ float factor_of(double norm, double max_norm) {
   const double f = max_norm / (norm + kClipEps);
-  return f > 1.0 ? 1.f : (float)f;     // NaN stays NaN
+  return f > 1.0 || isinf(max_norm) ? 1.f : (float)f;     // NaN stays NaN, where clipping was asked for
 }
 
 __global__ void __launch_bounds__(kThreads)

@@ -380,24 +380,24 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       }
     }
     if (warp < 6) {
-    const int q = warp & 3;
-    const int o = mt * M8_BM + q * 32 + lane;
-    const bool ok = warp_all(mbar_wait(done, 0, abort_flag, 408));
-    tc_fence_after();
-    float* part = reinterpret_cast<float*>(smem);    // every stage has been read
-    if (ok) {
-      for (int n0 = 0; n0 < NT && t0 + n0 < tokens; n0 += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)n0, r);
-        tmem_ld_wait();
+      const int q = warp & 3;
+      const int o = mt * M8_BM + q * 32 + lane;
+      const bool ok = warp_all(mbar_wait(done, 0, abort_flag, 408));
+      tc_fence_after();
+      float* part = reinterpret_cast<float*>(smem);    // every stage has been read
+      if (ok) {
+        for (int n0 = 0; n0 < NT && t0 + n0 < tokens; n0 += 16) {
+          uint32_t r[16];
+          tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)n0, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = t0 + n0 + i;
-          if (S > 1) part[(n0 + i) * 128 + q * 32 + lane] = __uint_as_float(r[i]);
-          else if (t < tokens && o < cout) Y[(size_t)t * cout + o] = from_f32<OUT>(__uint_as_float(r[i]));
+          for (int i = 0; i < 16; ++i) {
+            const int t = t0 + n0 + i;
+            if (S > 1) part[(n0 + i) * 128 + q * 32 + lane] = __uint_as_float(r[i]);
+            else if (t < tokens && o < cout) Y[(size_t)t * cout + o] = from_f32<OUT>(__uint_as_float(r[i]));
+          }
         }
       }
-    }
     }
   }
   tc_fence_before();

@@ -589,5 +589,7 @@ def grad_norm(grads) -> float:
 
 
 def clip_factor(norm: float, max_norm: float) -> float:
-    f = max_norm / (norm + 1e-6) if np.isfinite(max_norm) else float("inf") if np.isfinite(norm) else float("nan")
+    if np.isinf(max_norm):
+        return 1.0
+    f = max_norm / (norm + 1e-6)
     return f if np.isnan(f) else min(1.0, f)

@@ -273,7 +273,7 @@ def test_linear8_is_the_quantiser_and_the_product(gpu_lib, xdt, T, cin, cout, B)
     assert b.device_error() == 0
 
 
-@pytest.mark.parametrize("T", [1, 2, 3, 6, 9, 16])
+@pytest.mark.parametrize("T", [1, 2, 3, 6, 9, 16, 19, 33, 64])
 @pytest.mark.parametrize("cin,cout,B", [(4096, 11008, 64), (2272, 19200, 32), (13824, 640, 256)])
 def test_linear8_few_tokens_over_many_groups(gpu_lib, T, cin, cout, B):
     """Ranges of channels several times the ring's length in one CTA, for every number of token pairs."""

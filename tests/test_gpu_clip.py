@@ -123,6 +123,27 @@ def test_a_norm_that_is_not_finite_is_passed_on(gpu_lib, value):
         assert n == float("inf") and bool(ts[0][77].isnan()) and float(ts[0].nansum()) == 0 and float(ts[1].sum()) == 0
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n", [1000, 300000])
+def test_no_limit_leaves_the_other_values_as_they_are(gpu_lib, value, n):
+    """An infinite max_norm asks for no clipping, whatever the norm: the bad value stays the only one."""
+    g = torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+    g[77] = value
+    small = torch.ones(3, dtype=torch.bfloat16, device="cuda")
+    out = [torch.zeros_like(g), torch.zeros_like(small)]
+    norm = float(b.GradList([g, small], out).clip(float("inf")))
+    assert not np.isfinite(norm)
+    keep = torch.arange(n, device="cuda") != 77
+    assert torch.equal(out[0][keep], g[keep]) and torch.equal(out[1], small) and not bool(out[0][77].isfinite())
+    opt = b.adamw_params()
+    one, other = [[torch.ones(n, device="cuda"), g.clone(), torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")]
+                  for _ in range(2)]
+    b.AdamwList(*[[t] for t in one]).run(opt, 1)
+    b.adamw(other[0], other[1], other[2], other[3], opt, 1)
+    for x, y in zip(one, other):
+        assert torch.equal(x[keep], y[keep])
+
+
 @pytest.mark.parametrize("scale", [1e30, 1e-30, 1e-42])
 def test_squares_neither_overflow_nor_vanish(gpu_lib, scale):
     ts = [torch.full((4099,), scale, device="cuda")]
