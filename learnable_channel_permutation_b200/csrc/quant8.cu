@@ -52,15 +52,59 @@ __device__ __forceinline__ void apply_mask(Vec8<__nv_bfloat16>& v, uint32_t keep
   }
 }
 
-// CTAs of the activation kernel that fit an SM.
-template <typename T, bool PERM> constexpr int row_ctas() { return sizeof(T) == 4 && PERM ? 3 : 4; }
+// How a kernel permutes.  Blocks of at most 128 channels keep every value in its scale group, so the
+// scale does not depend on the order and the e4m3 bytes can be moved (kBytes), four rows a word: the
+// exchange through shared memory, whose random accesses hit a bank three to four times a warp, is
+// half of bf16's and a quarter of float32's.  Blocks of 256 move the values before the groups' maxima
+// are taken (kValues).  As bytes and as values: 4096 x 13824 float32 activations 44 and 60 us,
+// 8192 x 11008 bf16 47 and 50; weights of 5120 x 13824, permuted 34 and 44, masked too 42 and 48, float32
+// 73 and 90.
+enum class Order { kPlain, kValues, kBytes };
 
-// Activations.  A warp keeps one 256-channel chunk and walks tokens two at a time, the next two
-// loading meanwhile, so the permutation is read once and its slots stay in registers.
-template <typename T, bool PERM>
-__global__ void __launch_bounds__(32 * Q8_ROW_WARPS, row_ctas<T, PERM>())
+// The same for values that are not permuted yet.  keep[0] holds the mask bytes of rows 0 to 3, keep[1] of rows 4
+// to 7, in the permuted order; g[j] becomes the bits, row r's in bit r, that source channel j meets
+// at its slot.  The eight bytes are transposed as 8 x 8 bits (by exchanging 1 x 1, then 2 x 2, then 4 x 4
+// squares across the diagonal), so a channel's byte is one random access, in 256 bytes that
+// lie at most two words to a bank.
+__device__ __forceinline__ void gather_mask(const uint32_t (&keep)[2], const uint32_t (&slot)[8], uint32_t* buf, int lane,
+                                            uint32_t (&g)[8]) {
+  uint32_t x = keep[1], y = keep[0], t;
+  t = (x ^ (x >> 7)) & 0x00aa00aau, x ^= t ^ (t << 7);
+  t = (y ^ (y >> 7)) & 0x00aa00aau, y ^= t ^ (t << 7);
+  t = (x ^ (x >> 14)) & 0x0000ccccu, x ^= t ^ (t << 14);
+  t = (y ^ (y >> 14)) & 0x0000ccccu, y ^= t ^ (t << 14);
+  reinterpret_cast<uint2*>(buf)[lane] = make_uint2((x << 4 & 0xf0f0f0f0u) | (y & 0x0f0f0f0fu),
+                                                   (x & 0xf0f0f0f0u) | (y >> 4 & 0x0f0f0f0fu));
+  __syncwarp();
+  const uint32_t base3 = 3u * static_cast<uint32_t>(__cvta_generic_to_shared(buf));
+#pragma unroll
+  for (int j = 0; j < 8; ++j)      // slot = base + 4 i, the byte is at base + i
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(g[j]) : "r"((slot[j] + base3) >> 2));
+}
+__device__ __forceinline__ void apply_mask_row(Vec8<float>& v, const uint32_t (&g)[8], int row) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (!(g[j] >> row & 1u)) w[j] = 0u;
+}
+__device__ __forceinline__ void apply_mask_row(Vec8<__nv_bfloat16>& v, const uint32_t (&g)[8], int row) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] &= byte_signs<0xaa88>((g[2 * j] | g[2 * j + 1] << 16) << (7 - row));
+}
+
+// CTAs of the activation kernel that fit an SM.
+template <typename T, Order ORDER> constexpr int row_ctas() { return sizeof(T) == 4 && ORDER != Order::kPlain ? 3 : 4; }
+
+// Activations.  A warp keeps one 256-channel chunk and walks tokens two at a time (four where it
+// moves bytes), the next two loading meanwhile, so the permutation is read once and its slots
+// stay in registers.
+template <typename T, Order ORDER>
+__global__ void __launch_bounds__(32 * Q8_ROW_WARPS, row_ctas<T, ORDER>())
 quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, uint8_t* __restrict__ Q,
                    uint8_t* __restrict__ S, int tokens, int cin, int bmask) {
+  constexpr bool PERM = ORDER != Order::kPlain;
+  constexpr int PAIRS = ORDER == Order::kBytes ? 2 : 1;      // of tokens a round
   __shared__ __align__(16) uint32_t stage[PERM ? Q8_ROW_WARPS : 1][PERM ? Q8_STAGE : 4];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int chan = blockIdx.x * Q8_CHUNK + 8 * lane;
@@ -74,36 +118,45 @@ quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, ui
   Vec8<T> next[2] = {load(t), load(t + step)};
   uint32_t slot[8];
   if (PERM) load_slots(perm, chan, lane, cin, bmask, stage[warp], slot, &g_quant_error);
-  for (; t < tokens; t += 2 * step) {
-    Vec8<T> v[2] = {next[0], next[1]};
-    next[0] = load(t + 2 * step);
-    next[1] = load(t + 3 * step);
-    if (PERM) permute_rows(v[0], v[1], slot, stage[warp], lane);
-    uint32_t m[2];
-    group_max(v, m);
+  for (; t < tokens; t += 2 * PAIRS * step) {
+    uint2 q[2 * PAIRS];
+    uint32_t byte[2 * PAIRS];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int h = 0; h < PAIRS; ++h) {
+      Vec8<T> v[2] = {next[0], next[1]};
+      next[0] = load(t + (2 * h + 2) * step);
+      next[1] = load(t + (2 * h + 3) * step);
+      if (ORDER == Order::kValues) permute_rows(v[0], v[1], slot, stage[warp], lane);
+      uint32_t m[2];
+      group_max(v, m);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        byte[2 * h + u] = scale_byte(m[u]);
+        q[2 * h + u] = to_e4m3(v[u], scale_inverse(byte[2 * h + u]));
+      }
+    }
+    if constexpr (ORDER == Order::kBytes) permute_bytes(q, slot, stage[warp], lane);
+#pragma unroll
+    for (int u = 0; u < 2 * PAIRS; ++u) {
       const int row = t + u * step;
       if (row >= tokens || !in) break;
-      const uint32_t byte = scale_byte(m[u]);
-      *reinterpret_cast<uint2*>(Q + (size_t)row * cin + chan) = to_e4m3(v[u], scale_inverse(byte));
-      if ((lane & 15) == 0) S[(size_t)row * G + chan / 128] = (uint8_t)byte;
+      *reinterpret_cast<uint2*>(Q + (size_t)row * cin + chan) = q[u];
+      if ((lane & 15) == 0) S[(size_t)row * G + chan / 128] = (uint8_t)byte[u];
     }
   }
 }
 
 // Weights.  A CTA takes 128 rows x CH channels and holds the values in registers (in their stored
 // type, 32 registers a lane) while the block maxima are reduced.  CH = 256 (two blocks, a warp to a
-// row) for B = 256 and for every permuted bf16 weight, 128 (half a warp to a row) otherwise:
-// smaller CTAs overlap their phases better (5120 x 13824 as it is: 32.2 us, 33.7 at CH = 256; float32
-// permuted: 90 us, 104), but bf16's exchange does not gain by it (permuted and masked: 49.7 us at
-// CH = 128, 47.3 at 256).
+// row) for B = 256, 128 (half a warp to a row) otherwise: smaller CTAs overlap their phases better
+// (5120 x 13824 permuted and masked: 41.6 us, 48.2 at CH = 256; as it is: 32.2 us, 33.7).
 template <typename T> constexpr int w_loads() { return 16 / (int)sizeof(T); }     // of a lane, each eight channels of a row
 template <typename T, int CH> constexpr int w_warps() { return CH / 2 / w_loads<T>(); }
-template <typename T, bool PERM, bool MASK, int CH>
+template <typename T, Order ORDER, bool MASK, int CH>
 __global__ void __launch_bounds__(32 * w_warps<T, CH>(), 32 / w_warps<T, CH>())
 quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, const uint8_t* __restrict__ mask,
                      uint8_t* __restrict__ Q, uint8_t* __restrict__ S, int cout, int cin, int bmask) {
+  constexpr bool PERM = ORDER != Order::kPlain;
   constexpr int LOADS = w_loads<T>(), WARPS = w_warps<T, CH>();
   constexpr int ROWS = 256 / CH;     // of a warp's load
   __shared__ __align__(16) uint32_t stage[PERM ? WARPS : 1][PERM ? Q8_STAGE : 4];
@@ -138,11 +191,14 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
   }
   uint32_t slot[8];
   if (PERM) load_slots(perm, chan, lane, cin, bmask, stage[warp], slot, &g_quant_error);
+  uint32_t g[8];
+  if (MASK && ORDER == Order::kBytes) gather_mask(keep, slot, stage[warp], lane, g);
   uint32_t m = 0;
 #pragma unroll
   for (int r = 0; r < LOADS; ++r) {
-    if (PERM && r % 2 == 0) permute_rows(v[r], v[r + 1], slot, stage[warp], lane);
-    if (MASK) apply_mask(v[r], keep[r / 4] >> (8 * (r % 4)));
+    if (ORDER == Order::kValues && r % 2 == 0) permute_rows(v[r], v[r + 1], slot, stage[warp], lane);
+    if (MASK && ORDER == Order::kBytes) apply_mask_row(v[r], g, r);
+    else if (MASK) apply_mask(v[r], keep[r / 4] >> (8 * (r % 4)));
     m = max(m, amax8(v[r]));
   }
   m = half_max(m);
@@ -153,47 +209,56 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
   for (int w = 0; w < WARPS; ++w) m = max(m, CH == 128 ? max(part[w][0], part[w][1]) : part[w][lane >> 4]);
   const uint32_t byte = scale_byte(m);
   const float inv = scale_inverse(byte);
-  if (!in) return;
   uint8_t* q0 = Q + (size_t)o0 * cin + chan;
 #pragma unroll
-  for (int r = 0; r < LOADS; ++r)
-    if (whole || o0 + r * WARPS * ROWS < cout) *reinterpret_cast<uint2*>(q0 + r * step) = to_e4m3(v[r], inv);
-  if (warp == 0 && (lane == 0 || (CH == 256 && lane == 16))) S[(size_t)blockIdx.y * G + chan / 128] = (uint8_t)byte;
+  for (int r0 = 0; r0 < LOADS; r0 += 4) {
+    uint2 q[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) q[r] = to_e4m3(v[r0 + r], inv);
+    if constexpr (ORDER == Order::kBytes) permute_bytes(q, slot, stage[warp], lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (whole || (in && o0 + (r0 + r) * WARPS * ROWS < cout)) *reinterpret_cast<uint2*>(q0 + (r0 + r) * step) = q[r];
+  }
+  if (in && warp == 0 && (lane == 0 || (CH == 256 && lane == 16))) S[(size_t)blockIdx.y * G + chan / 128] = (uint8_t)byte;
 }
 
 int cdiv_host(int a, int b) { return (a + b - 1) / b; }
 
-template <typename T>
+// As many CTAs a chunk as fit the GPU at once (one more would cost a second round of all of them).
+template <typename T, Order ORDER> int row_fit(int cin) {
+  return std::max(row_ctas<T, ORDER>() * device_sms() / cdiv_host(cin, Q8_CHUNK), 1);
+}
+template <typename T, Order ORDER>
 lcp_status rows_t(const T* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B, cudaStream_t st) {
-  const int sms = device_sms(), chunks = cdiv_host(cin, Q8_CHUNK);
-  // as many CTAs as fit the GPU at once (one more would cost a second round of all of them)
-  const int fit = (perm ? row_ctas<T, true>() : row_ctas<T, false>()) * sms / chunks;
-  const int gy = std::min(cdiv_host(tokens, Q8_ROW_WARPS), std::max(fit, 1));
-  const dim3 grid((unsigned)chunks, (unsigned)gy);
-  const int bmask = perm ? B - 1 : 0;
-  if (perm)
-    return launch_kernel(quant8_rows_kernel<T, true>, grid, dim3(32 * Q8_ROW_WARPS), 0, st, 1, true, "quant8", X, perm, Q,
-                         S, tokens, cin, bmask);
-  return launch_kernel(quant8_rows_kernel<T, false>, grid, dim3(32 * Q8_ROW_WARPS), 0, st, 1, true, "quant8", X, perm, Q, S,
-                       tokens, cin, bmask);
+  const int chunks = cdiv_host(cin, Q8_CHUNK);
+  const int gy = std::min(cdiv_host(tokens, Q8_ROW_WARPS), row_fit<T, ORDER>(cin));
+  return launch_kernel(quant8_rows_kernel<T, ORDER>, dim3((unsigned)chunks, (unsigned)gy), dim3(32 * Q8_ROW_WARPS), 0, st, 1,
+                       true, "quant8", X, perm, Q, S, tokens, cin, B - 1);
+}
+template <typename T>
+lcp_status rows_order(const T* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B, cudaStream_t st) {
+  if (!perm) return rows_t<T, Order::kPlain>(X, perm, Q, S, tokens, cin, 1, st);
+  // bf16 of at most two tokens a warp: a round of the byte order is four (512 x 4096: 2.8 us, 3.5 as bytes)
+  const bool few = sizeof(T) == 2 && tokens <= 2 * Q8_ROW_WARPS * row_fit<T, Order::kValues>(cin);
+  if (B == 256 || few) return rows_t<T, Order::kValues>(X, perm, Q, S, tokens, cin, B, st);
+  return rows_t<T, Order::kBytes>(X, perm, Q, S, tokens, cin, B, st);
 }
 
-template <typename T, bool PERM, int CH>
+template <typename T, Order ORDER, int CH>
 lcp_status weight_ch(const T* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S, int cout, int cin,
                      int B, cudaStream_t st) {
   const dim3 grid((unsigned)cdiv_host(cin, CH), (unsigned)cdiv_host(cout, 128)), block(32 * w_warps<T, CH>());
   const uint8_t* mb = reinterpret_cast<const uint8_t*>(mask);
-  const auto kernel = mask ? quant8_weight_kernel<T, PERM, true, CH> : quant8_weight_kernel<T, PERM, false, CH>;
+  const auto kernel = mask ? quant8_weight_kernel<T, ORDER, true, CH> : quant8_weight_kernel<T, ORDER, false, CH>;
   return launch_kernel(kernel, grid, block, 0, st, 1, true, "quant8_weight", W, perm, mb, Q, S, cout, cin, B - 1);
 }
 template <typename T>
 lcp_status weight_t(const T* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S, int cout, int cin,
                     int B, cudaStream_t st) {
-  if (!perm) return weight_ch<T, false, 128>(W, perm, mask, Q, S, cout, cin, 1, st);
-  if constexpr (sizeof(T) == 4) {
-    if (B != 256) return weight_ch<T, true, 128>(W, perm, mask, Q, S, cout, cin, B, st);
-  }
-  return weight_ch<T, true, 256>(W, perm, mask, Q, S, cout, cin, B, st);
+  if (!perm) return weight_ch<T, Order::kPlain, 128>(W, perm, mask, Q, S, cout, cin, 1, st);
+  if (B == 256) return weight_ch<T, Order::kValues, 256>(W, perm, mask, Q, S, cout, cin, B, st);
+  return weight_ch<T, Order::kBytes, 128>(W, perm, mask, Q, S, cout, cin, B, st);
 }
 
 }  // namespace
@@ -215,8 +280,8 @@ lcp_status quant_error(int* site, int reset) {
 
 lcp_status launch_quant8(const void* X, const int32_t* perm, uint8_t* Q, uint8_t* S, int tokens, int cin, int B,
                          lcp_dtype dt, cudaStream_t st) {
-  if (dt == LCP_F32) return rows_t(static_cast<const float*>(X), perm, Q, S, tokens, cin, B, st);
-  return rows_t(static_cast<const __nv_bfloat16*>(X), perm, Q, S, tokens, cin, B, st);
+  if (dt == LCP_F32) return rows_order(static_cast<const float*>(X), perm, Q, S, tokens, cin, B, st);
+  return rows_order(static_cast<const __nv_bfloat16*>(X), perm, Q, S, tokens, cin, B, st);
 }
 
 lcp_status launch_quant8_weight(const void* W, const int32_t* perm, const uint32_t* mask, uint8_t* Q, uint8_t* S,

@@ -177,5 +177,35 @@ __device__ __forceinline__ uint2 to_e4m3(const Vec8<__nv_bfloat16>& v, float inv
   return make_uint2(pair_e4m3(w[0], i2) | (pair_e4m3(w[1], i2) << 16), pair_e4m3(w[2], i2) | (pair_e4m3(w[3], i2) << 16));
 }
 
+// 4 x 4 bytes: word i byte k <-> word k byte i.
+__device__ __forceinline__ void transpose_bytes(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  const uint32_t t0 = __byte_perm(a, b, 0x5140), t1 = __byte_perm(a, b, 0x7362);
+  const uint32_t t2 = __byte_perm(c, d, 0x5140), t3 = __byte_perm(c, d, 0x7362);
+  a = __byte_perm(t0, t2, 0x5410);
+  b = __byte_perm(t0, t2, 0x7632);
+  c = __byte_perm(t1, t3, 0x5410);
+  d = __byte_perm(t1, t3, 0x7632);
+}
+// Moves four rows' eight e4m3 values of every lane to their slots: the rows' bytes of a channel
+// share a word, so one 4-byte store moves four.
+__device__ __forceinline__ void permute_bytes(uint2* q, const uint32_t (&slot)[8], const uint32_t* buf, int lane) {
+  transpose_bytes(q[0].x, q[1].x, q[2].x, q[3].x);
+  transpose_bytes(q[0].y, q[1].y, q[2].y, q[3].y);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    st_shared(slot[j], q[j].x);
+    st_shared(slot[4 + j], q[j].y);
+  }
+  __syncwarp();
+  uint32_t w[8];
+  *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(buf + 8 * lane)[0];
+  *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(buf + 8 * lane)[1];
+  transpose_bytes(w[0], w[1], w[2], w[3]);
+  transpose_bytes(w[4], w[5], w[6], w[7]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q[j] = make_uint2(w[j], w[4 + j]);
+}
+
 }  // namespace
 }  // namespace lcp

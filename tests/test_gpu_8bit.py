@@ -118,6 +118,39 @@ def test_quant8_weight_ignores_what_the_mask_drops(gpu_lib):
     assert _same(_np(q), rq) and _same(_np(s), rs)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,cin,B", [(231, 11040, 32), (300, 11072, 64), (451, 11136, 128), (215, 13824, 256)])
+def test_quant8_many_tokens_a_warp(gpu_lib, dtype, T, cin, B):
+    """Several rounds of four tokens, the last one not whole, with infinities and NaN in some groups."""
+    rng = np.random.default_rng(T + cin)
+    X = _rows(rng, T, cin, dtype)
+    X[5, 700], X[T - 1, cin - 1], X[T // 2, 40] = float("inf"), float("nan"), -float("inf")
+    perm = _perm(rng, cin, B)
+    q, s = b.quant8(X.cuda(), _dev_perm(perm))
+    rq, rs = O.quant8(_np(X), perm)
+    assert _same(_np(q), rq) and _same(_np(s), rs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cout,cin,B", [(255, 1184, 32), (385, 1216, 64), (129, 1408, 128), (130, 512, 256), (3, 32, 32)])
+def test_quant8_weight_any_mask_under_a_permutation(gpu_lib, dtype, cout, cin, B):
+    """Masks of no pattern, whole rows and blocks dropped, infinities and NaN in dropped and in kept places."""
+    rng = np.random.default_rng(cout + cin)
+    perm = _perm(rng, cin, B)
+    A = rng.normal(size=(cout, cin)) * np.exp2(rng.integers(-6, 6, size=(1, cin)))
+    M = rng.random((cout, cin)) < rng.random((cout, 1))
+    M[cout // 2] = False
+    M[:128, :32] = False
+    A[~M] = rng.choice([np.inf, -np.inf, np.nan, 1e30, 1.0], size=int((~M).sum()))
+    if cout > 128:
+        A[-1, -1], M[-1, -1] = np.inf, True
+    W = torch.from_numpy(O.gather_channels(A, np.argsort(perm, axis=1))).to(DT[dtype])       # A = W P_B
+    q, s = b.quant8_weight(W.cuda(), _dev_perm(perm), torch.from_numpy(O.pack_mask_bits(M).view(np.int32)).cuda())
+    rq, rs = O.quant8_weight(_np(W), perm, M)
+    assert _same(_np(q), rq) and _same(_np(s), rs)
+    assert np.isnan(rs).sum() == (1 if cout > 128 else 0)
+
+
 def test_quant8_reports_an_invalid_permutation_entry(gpu_lib):
     perm = torch.arange(32, dtype=torch.int32).repeat(4, 1).cuda()
     perm[2, 5] = 32
