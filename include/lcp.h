@@ -436,7 +436,7 @@ LCP_API lcp_status lcp_sparse24_mm(const void* values, const uint32_t* meta, con
  * G = ceil(C_in / 128) groups of channels; a last group or block that is not
  * whole holds what there is.  C_in a multiple of 32; with perm also of B, B in
  * {32, 64, 128, 256}.  perm as for lcp_gather; an entry outside [0, B) is
- * skipped and recorded in lcp_device_error (302), and like any perm that is not
+ * recorded in lcp_device_error (302), and like any perm that is not
  * a permutation of its block leaves unspecified values.  Outputs must not
  * overlap inputs. */
 

@@ -57,8 +57,8 @@ __device__ __forceinline__ void apply_mask(Vec8<__nv_bfloat16>& v, uint32_t keep
 // exchange through shared memory, whose random accesses hit a bank three to four times a warp, is
 // half of bf16's and a quarter of float32's.  Blocks of 256 move the values before the groups' maxima
 // are taken (kValues).  As bytes and as values: 4096 x 13824 float32 activations 44 and 60 us,
-// 8192 x 11008 bf16 47 and 50; weights of 5120 x 13824, permuted 34 and 44, masked too 42 and 48, float32
-// 73 and 90.
+// 8192 x 11008 bf16 47 and 50; weights of 5120 x 13824, permuted 34 and 44, masked too 41 and 48, float32
+// 70 and 90.
 enum class Order { kPlain, kValues, kBytes };
 
 // The same for values that are not permuted yet.  keep[0] holds the mask bytes of rows 0 to 3, keep[1] of rows 4
@@ -93,8 +93,11 @@ __device__ __forceinline__ void apply_mask_row(Vec8<__nv_bfloat16>& v, const uin
   for (int j = 0; j < 4; ++j) w[j] &= byte_signs<0xaa88>((g[2 * j] | g[2 * j + 1] << 16) << (7 - row));
 }
 
-// CTAs of the activation kernel that fit an SM.
-template <typename T, Order ORDER> constexpr int row_ctas() { return sizeof(T) == 4 && ORDER != Order::kPlain ? 3 : 4; }
+// CTAs of the activation kernel that fit an SM (bf16 of 8192 x 11008 as it is: 42 us with five, 46 with
+// four; permuted: 47 with four, 50 with five, 61 with three).
+template <typename T, Order ORDER> constexpr int row_ctas() {
+  return (sizeof(T) == 4 ? 3 : 4) + (ORDER == Order::kPlain ? 1 : 0);
+}
 
 // Activations.  A warp keeps one 256-channel chunk and walks tokens two at a time (four where it
 // moves bytes), the next two loading meanwhile, so the permutation is read once and its slots
@@ -149,7 +152,7 @@ quant8_rows_kernel(const T* __restrict__ X, const int32_t* __restrict__ perm, ui
 // Weights.  A CTA takes 128 rows x CH channels and holds the values in registers (in their stored
 // type, 32 registers a lane) while the block maxima are reduced.  CH = 256 (two blocks, a warp to a
 // row) for B = 256, 128 (half a warp to a row) otherwise: smaller CTAs overlap their phases better
-// (5120 x 13824 permuted and masked: 41.6 us, 48.2 at CH = 256; as it is: 32.2 us, 33.7).
+// (5120 x 13824 permuted and masked: 41 us, 48 at CH = 256; as it is: 32 us, 34).
 template <typename T> constexpr int w_loads() { return 16 / (int)sizeof(T); }     // of a lane, each eight channels of a row
 template <typename T, int CH> constexpr int w_warps() { return CH / 2 / w_loads<T>(); }
 template <typename T, Order ORDER, bool MASK, int CH>
@@ -199,9 +202,9 @@ quant8_weight_kernel(const T* __restrict__ W, const int32_t* __restrict__ perm, 
     if (ORDER == Order::kValues && r % 2 == 0) permute_rows(v[r], v[r + 1], slot, stage[warp], lane);
     if (MASK && ORDER == Order::kBytes) apply_mask_row(v[r], g, r);
     else if (MASK) apply_mask(v[r], keep[r / 4] >> (8 * (r % 4)));
-    m = max(m, amax8(v[r]));
+    m = fold_max(m, v[r]);
   }
-  m = half_max(m);
+  m = half_max(max_bits<T>(m));
   if ((lane & 15) == 0) part[warp][lane >> 4] = m;
   __syncthreads();
   m = 0;

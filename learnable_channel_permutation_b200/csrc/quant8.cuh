@@ -46,30 +46,29 @@ template <typename T> __device__ __forceinline__ Vec8<T> zero8() {
   return r;
 }
 
-constexpr int Q8_STAGE = Q8_CHUNK + 4;   // words of a warp's exchange buffer; word 256 takes what has no slot
+constexpr int Q8_STAGE = Q8_CHUNK;   // words of a warp's exchange buffer
 
 // Where a lane's eight source channels of the warp's chunk go in the exchange buffer (shared
-// addresses): word 256 for a permutation entry outside [0, B); their own places past the last
-// channel (their zeros are moved like values, so that every slot is written).  A bad entry is
-// recorded in *error.
+// addresses): their own places past the last channel (their zeros are moved like values, so that
+// every slot is written).  An entry outside [0, B) is recorded in *error, and its low bits are taken, which
+// keeps every slot in its block.
 __device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int lane, int cin, int bmask,
                                            const uint32_t* buf, uint32_t (&slot)[8], int* error) {
-  int4 p[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+  const uint32_t own = 8u * (uint32_t)lane, mask = (uint32_t)bmask;
+  uint32_t e[8];
   if (chan < cin) {
-    p[0] = __ldg(reinterpret_cast<const int4*>(perm + chan));
-    p[1] = __ldg(reinterpret_cast<const int4*>(perm + chan) + 1);
-  }
-  const int* e = reinterpret_cast<const int*>(p);
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(buf));
-  bool bad = false;
+    const uint4* at = reinterpret_cast<const uint4*>(perm + chan);
+    const uint4 p = __ldg(at), q = __ldg(at + 1);
+    e[0] = p.x, e[1] = p.y, e[2] = p.z, e[3] = p.w, e[4] = q.x, e[5] = q.y, e[6] = q.z, e[7] = q.w;
+    if ((e[0] | e[1] | e[2] | e[3] | e[4] | e[5] | e[6] | e[7]) & ~mask) atomicCAS(error, 0, 302);
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int own = 8 * lane + j;
-    const bool out = (unsigned)e[j] > (unsigned)bmask;
-    bad |= out;
-    slot[j] = base + 4u * (uint32_t)(chan >= cin ? own : (out ? Q8_CHUNK : (own & ~bmask) | e[j]));
+    for (int j = 0; j < 8; ++j) e[j] = own + (uint32_t)j;
   }
-  if (bad) atomicCAS(error, 0, 302);
+  // blocks are at least 32 wide: a lane's eight channels share the bits above the block's
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(buf)), block = own & ~mask;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) slot[j] = base + 4u * (block | (e[j] & mask));
 }
 __device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -113,31 +112,30 @@ __device__ __forceinline__ void permute_rows(Vec8<T>& a, Vec8<T>& b, const uint3
   }
 }
 
-// Largest magnitude of eight values, as float bits (infinities above every finite value and NaNs
-// above those, as integers compare).  bf16 pairs are compared as they are stored.
-__device__ __forceinline__ uint32_t amax8(const Vec8<float>& v) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7fffffffu);
-  return m;
-}
-// a bf16 pair's maxima; a NaN wins
+// Largest magnitudes.  A fold takes eight values into a running maximum (0 to begin with); a NaN wins.
+// float32: its bits, two values an instruction.  bf16: two running maxima in a word (its
+// instruction that takes magnitudes itself measured slower: 8192 x 11008 permuted 49 us, 47).
 __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t amax_pair(const Vec8<__nv_bfloat16>& v) {
+__device__ __forceinline__ uint32_t fold_max(uint32_t m, const Vec8<__nv_bfloat16>& v) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-  uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int j = 1; j < 4; ++j) m = max_pair(m, w[j] & 0x7fff7fffu);
+  for (int j = 0; j < 4; ++j) m = max_pair(m, w[j] & 0x7fff7fffu);
   return m;
 }
-__device__ __forceinline__ uint32_t amax8(const Vec8<__nv_bfloat16>& v) {
-  const uint32_t m = amax_pair(v);
-  return max(m << 16, m & 0xffff0000u);
+__device__ __forceinline__ uint32_t fold_max(uint32_t m, const Vec8<float>& v) {
+  const float* f = reinterpret_cast<const float*>(&v);
+  float x = __uint_as_float(m);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(x) : "f"(f[j]), "f"(f[j + 1]));
+  return __float_as_uint(x);
+}
+// the maximum as float bits: infinities above every finite value and NaNs above those, as integers compare
+template <typename T> __device__ __forceinline__ uint32_t max_bits(uint32_t m) {
+  return sizeof(T) == 4 ? m : max(m << 16, m & 0xffff0000u);
 }
 // over the 16 lanes that share a scale group
 __device__ __forceinline__ uint32_t half_max(uint32_t m) {
@@ -147,11 +145,11 @@ __device__ __forceinline__ uint32_t half_max(uint32_t m) {
 }
 // The group maxima of two rows (bf16: both travel in one word).
 __device__ __forceinline__ void group_max(const Vec8<float> (&v)[2], uint32_t (&m)[2]) {
-  m[0] = half_max(amax8(v[0]));
-  m[1] = half_max(amax8(v[1]));
+  m[0] = half_max(fold_max(0u, v[0]));
+  m[1] = half_max(fold_max(0u, v[1]));
 }
 __device__ __forceinline__ void group_max(const Vec8<__nv_bfloat16> (&v)[2], uint32_t (&m)[2]) {
-  const uint32_t a = amax_pair(v[0]), b = amax_pair(v[1]);
+  const uint32_t a = fold_max(0u, v[0]), b = fold_max(0u, v[1]);
   uint32_t w = max_pair(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) w = max_pair(w, __shfl_xor_sync(0xffffffffu, w, o));
