@@ -116,8 +116,8 @@ constexpr int M8_BM = 128;            // output channels of a CTA: one row of we
 constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one scale group of channels)
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
 constexpr int M8_FUSED_TOKENS = 8;    // plain activations of up to so many tokens are quantised by the product itself
-                                      // (16 tokens x 4096 x 11008: 18.2 us, 13.2 as two launches; 8 tokens: 12.5)
-constexpr int M8_FUSED_WARPS = 8;     // warps that do (16 leave one CTA an SM: 16.2 us instead of 6.9 at 4096 x 4096)
+                                      // (8 tokens x 4096 x 11008: 12.3 us; 16: 17.0, 13.2 as two launches)
+constexpr int M8_FUSED_WARPS = 8;     // warps that do (16 leave one CTA an SM: 16.2 us, 6.9 then, at 4096 x 4096)
 // warp 0: TMA, 1: MMA, 2-5: epilogue; 6: scales, or all from 2 on: quantisers
 template <typename XT> constexpr int m8_threads() { return sizeof(XT) == 1 ? 224 : 64 + 32 * M8_FUSED_WARPS; }
 constexpr int M8_MAX_STAGES = 12;
@@ -155,8 +155,8 @@ template <typename OUT> __device__ __forceinline__ void store4(OUT* out, const f
 // builds the scale words.  XT = float or bf16 (at most 8 tokens): X holds the activations
 // themselves, and eight warps quantise the CTA's channels (permuted, if PERM) straight into the
 // tiles and scale words.  Every CTA of a column of tiles quantises the same tokens again, 8 at
-// the most: that costs less than a launch that does it once (one token x 4096 x 4096: 8.0 us as
-// two launches).
+// the most: that costs less than a launch that does it once (one token x 4096 x 4096: 6.4 us, 8.0
+// as two launches).
 template <typename OUT, typename XT, bool PERM>
 __global__ void __launch_bounds__(m8_threads<XT>())
 mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -314,7 +314,8 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   } else {
     if constexpr (FUSED) {
       // Warps from 2 on: warp w takes the pair of tokens w % npp (npp: npairs rounded up to a power of two) and
-      // every `every`-th pair of groups, the next one's values loading meanwhile.  At most M8_FUSED_WARPS / npp warps
+      // every `every`-th pair of groups, the next one's values, permutation and scales of W loading meanwhile
+      // (5 to 12 % of the kernel's time at one token; two ahead measured no better).  At most M8_FUSED_WARPS / npp warps
       // share a pair of tokens, and no more than stages / 2: a warp that waits for a tile knows from its
       // own wait before, 2 every groups back, that the tile's use before the last is over, so the parity
       // it waits for cannot be an older phase's.
@@ -331,17 +332,30 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         const int chan = (g0 + 2 * p) * 128 + 8 * lane;
         return 2 * p < nk && chan < cin && row0 + u < tokens ? load8(X + (size_t)(row0 + u) * cin + chan) : zero8<XT>();
       };
+      const auto scales = [&](int p) {      // W's two scale bytes
+        const uint8_t* ws = Ws + (size_t)mt * G + g0 + 2 * p;
+        return pair == 0 && 2 * p < nk ? (uint32_t)__ldg(ws) | (2 * p + 1 < nk ? (uint32_t)__ldg(ws + 1) : 127u) << 8 : 0u;
+      };
+      const auto entries = [&](int p) {
+        return PERM ? load_perm(perm, 2 * p < nk ? (g0 + 2 * p) * 128 + 8 * lane : cin, lane, cin) : Perm8{};
+      };
       int p = pair < npairs && w / npp < every ? w / npp : 2 * nchunk;
       Vec8<XT> next[2] = {load(p, 0), load(p, 1)};
+      Perm8 next_perm = entries(p);
+      uint32_t next_scales = scales(p);
       for (; p < 2 * nchunk; p += every) {
         Vec8<XT> v[2] = {next[0], next[1]};
+        const Perm8 places = next_perm;
+        const uint32_t a = next_scales;
         next[0] = load(p + every, 0);
         next[1] = load(p + every, 1);
+        next_perm = entries(p + every);
+        next_scales = scales(p + every);
         const int c = p / 2, slot = c % M8_SF, chan = (g0 + 2 * p) * 128 + 8 * lane;
         if (2 * p < nk) {
           if (PERM) {
             uint32_t to[8];
-            load_slots(perm, chan, lane, cin, bmask, buf, to, &g_tc_error);
+            perm_slots(places, chan < cin, lane, bmask, buf, to, &g_tc_error);
             permute_rows(v[0], v[1], to, buf, lane);
           }
           uint32_t m[2];
@@ -364,8 +378,6 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             if ((lane & 15) == 0) words[512 + row * 16 + 2 * (p & 1) + (lane >> 4)] = (uint8_t)byte;
           }
           if (pair == 0) {
-            const uint8_t* ws = Ws + (size_t)mt * G + g0 + 2 * p;
-            const uint32_t a = (uint32_t)__ldg(ws) | (2 * p + 1 < nk ? (uint32_t)__ldg(ws + 1) : 127u) << 8;
 #pragma unroll
             for (int j = 0; j < 4; ++j) *reinterpret_cast<uint16_t*>(words + lane * 16 + 4 * j + 2 * (p & 1)) = (uint16_t)a;
           }

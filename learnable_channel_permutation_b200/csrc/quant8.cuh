@@ -48,27 +48,36 @@ template <typename T> __device__ __forceinline__ Vec8<T> zero8() {
 
 constexpr int Q8_STAGE = Q8_CHUNK;   // words of a warp's exchange buffer
 
-// Where a lane's eight source channels of the warp's chunk go in the exchange buffer (shared
-// addresses): their own places past the last channel (their zeros are moved like values, so that
-// every slot is written).  An entry outside [0, B) is recorded in *error, and its low bits are taken, which
-// keeps every slot in its block.
-__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int lane, int cin, int bmask,
-                                           const uint32_t* buf, uint32_t (&slot)[8], int* error) {
-  const uint32_t own = 8u * (uint32_t)lane, mask = (uint32_t)bmask;
-  uint32_t e[8];
+// The permutation entries of a lane's eight source channels; past the last channel, those that keep
+// every place (the zeros there are moved like values, so that every slot is written).
+struct __align__(16) Perm8 { uint32_t e[8]; };
+__device__ __forceinline__ Perm8 load_perm(const int32_t* __restrict__ perm, int chan, int lane, int cin) {
+  Perm8 r;
   if (chan < cin) {
     const uint4* at = reinterpret_cast<const uint4*>(perm + chan);
-    const uint4 p = __ldg(at), q = __ldg(at + 1);
-    e[0] = p.x, e[1] = p.y, e[2] = p.z, e[3] = p.w, e[4] = q.x, e[5] = q.y, e[6] = q.z, e[7] = q.w;
-    if ((e[0] | e[1] | e[2] | e[3] | e[4] | e[5] | e[6] | e[7]) & ~mask) atomicCAS(error, 0, 302);
+    *reinterpret_cast<uint4*>(r.e) = __ldg(at);
+    *reinterpret_cast<uint4*>(r.e + 4) = __ldg(at + 1);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = own + (uint32_t)j;
+    for (int j = 0; j < 8; ++j) r.e[j] = 8u * (uint32_t)lane + (uint32_t)j;
   }
+  return r;
+}
+// Where those channels go in the exchange buffer (shared addresses).  An entry outside [0, B) is
+// recorded in *error, and its low bits are taken, which keeps every slot in its block.
+__device__ __forceinline__ void perm_slots(const Perm8& p, bool in, int lane, int bmask, const uint32_t* buf,
+                                           uint32_t (&slot)[8], int* error) {
   // blocks are at least 32 wide: a lane's eight channels share the bits above the block's
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(buf)), block = own & ~mask;
+  const uint32_t* e = p.e;
+  const uint32_t mask = (uint32_t)bmask, block = 8u * (uint32_t)lane & ~mask;
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(buf));
+  if (in && ((e[0] | e[1] | e[2] | e[3] | e[4] | e[5] | e[6] | e[7]) & ~mask)) atomicCAS(error, 0, 302);
 #pragma unroll
   for (int j = 0; j < 8; ++j) slot[j] = base + 4u * (block | (e[j] & mask));
+}
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ perm, int chan, int lane, int cin, int bmask,
+                                           const uint32_t* buf, uint32_t (&slot)[8], int* error) {
+  perm_slots(load_perm(perm, chan, lane, cin), chan < cin, lane, bmask, buf, slot, error);
 }
 __device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
