@@ -119,6 +119,21 @@ def test_quant8_weight_ignores_what_the_mask_drops(gpu_lib):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [0, 64, 256])
+def test_subnormal_blocks(gpu_lib, dtype, B):
+    """Blocks whose every value is subnormal in the input's type, beside blocks that hold one normal value."""
+    rng = np.random.default_rng(B + 3)
+    tiny = torch.finfo(DT[dtype]).tiny
+    X = torch.from_numpy(rng.uniform(-1, 1, (140, 512)) * tiny * 0.99).to(DT[dtype])
+    X[::3, 300] = 2.0 * tiny
+    X[::5, 100] = 1.0
+    perm = _perm(rng, 512, B)
+    for q, s, rq, rs in ((*b.quant8(X.cuda(), _dev_perm(perm)), *O.quant8(_np(X), perm)),
+                         (*b.quant8_weight(X.cuda(), _dev_perm(perm)), *O.quant8_weight(_np(X), perm))):
+        assert _same(_np(q), rq) and _same(_np(s), rs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,cin,B", [(231, 11040, 32), (300, 11072, 64), (451, 11136, 128), (215, 13824, 256)])
 def test_quant8_many_tokens_a_warp(gpu_lib, dtype, T, cin, B):
     """Several rounds of four tokens, the last one not whole, with infinities and NaN in some groups."""
