@@ -292,10 +292,23 @@ def _check_disjoint(spans) -> None:
 
 def _list_device(tensors) -> torch.device:
     """The one CUDA device of a list of tensors (the current one for an empty list)."""
-    devs = {t.device for t in tensors}
+    devs = {t.get_device() for t in tensors}
     if len(devs) > 1:
         raise ValueError("tensors of one list must be on one device")
-    return devs.pop() if devs else torch.device("cuda", torch.cuda.current_device())
+    index = devs.pop() if devs else torch.cuda.current_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors")
+    return torch.device("cuda", index)
+
+
+def _addresses(tensors, dtypes, name: str) -> List[int]:
+    """The addresses of contiguous tensors of the given types."""
+    for t in tensors:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    return [t.data_ptr() for t in tensors]
 
 
 class _TensorList:
@@ -329,16 +342,18 @@ class GradList(_TensorList):
         if len(self.out) != len(self.grads):
             raise ValueError("one output per gradient")
         device = _list_device(self.grads + self.out)
-        items, spans = [], []
-        for g, o in zip(self.grads, self.out):
-            if o.dtype != g.dtype or o.shape != g.shape:
+        p = q = _addresses(self.grads, (torch.float32, torch.bfloat16), "grad")
+        n, dt = [g.numel() for g in self.grads], [_dt(g) for g in self.grads]
+        size = [4 * k if d == F32 else 2 * k for k, d in zip(n, dt)]
+        spans = list(zip(p, size))
+        if out is not None:
+            if any(o.dtype != g.dtype or o.shape != g.shape for g, o in zip(self.grads, self.out)):
                 raise ValueError("an output has the dtype and shape of its gradient")
-            p, q, size = _ptr(g, None, "grad"), _ptr(o, None, "out"), g.numel() * g.element_size()
-            items.append(LcpGrad(p, q, g.numel(), _dt(g)))
-            spans += [(p, size)] if p == q else [(p, size), (q, size)]
+            q = _addresses(self.out, (torch.float32, torch.bfloat16), "out")
+            spans += [(b_, k) for a, b_, k in zip(p, q, size) if a != b_]
         _check_disjoint(spans)
-        self.arr = (LcpGrad * max(1, len(items)))(*items)
-        self._prepare(len(items), device)
+        self.arr = (LcpGrad * max(1, len(p)))(*zip(p, q, n, dt))
+        self._prepare(len(p), device)
 
     def norm(self, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         return self._call(lib().lcp_grad_norm, stream=stream)
@@ -358,16 +373,14 @@ class AdamwList(_TensorList):
         if len({len(x) for x in self.tensors}) != 1:
             raise ValueError("L, dL, m and v must be lists of one length")
         device = _list_device([t for x in self.tensors for t in x])
-        items, spans = [], []
-        for group in zip(*self.tensors):
-            if len({t.numel() for t in group}) != 1:
-                raise ValueError("a parameter, its gradient and its moments have one size")
-            ptrs = [_ptr(t, torch.float32, name) for t, name in zip(group, ("L", "dL", "m", "v"))]
-            items.append(LcpAdamwTensor(*ptrs, group[0].numel()))
-            spans += [(p, 4 * group[0].numel()) for p in ptrs]
-        _check_disjoint(spans)
-        self.arr = (LcpAdamwTensor * max(1, len(items)))(*items)
-        self._prepare(len(items), device)
+        n = [t.numel() for t in self.tensors[0]]
+        if any([t.numel() for t in x] != n for x in self.tensors[1:]):
+            raise ValueError("a parameter, its gradient and its moments have one size")
+        ptrs = [_addresses(x, (torch.float32,), name) for x, name in zip(self.tensors, ("L", "dL", "m", "v"))]
+        size = [4 * k for k in n]
+        _check_disjoint([span for p in ptrs for span in zip(p, size)])
+        self.arr = (LcpAdamwTensor * max(1, len(n)))(*zip(*ptrs, n))
+        self._prepare(len(n), device)
 
     def run(self, opt: LcpAdamwParams, t: int, max_norm: float = float("inf"),
             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
