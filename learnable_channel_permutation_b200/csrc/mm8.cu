@@ -640,13 +640,15 @@ mm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const uint32_t sffull0 = mapa(sffull(0), 0);
     uint32_t ss = 0, par = 0;
     bool ok = true;
-    for (int it = pair; it < total && ok; it += npairs, par ^= 1u) {
+    for (int it = pair; it < total; it += npairs, par ^= 1u) {
+      // The four warps are done with the tile before, and they leave together once a wait of any of them has
+      // given up: a warp that left alone would keep the others at the barrier, which has no limit.
+      if (!named_and(1, 128, ok)) break;
       int mt, nt;
       tile_at(it, mt, nt);
       const int wblock = 2 * mt + (int)rank, rows = min(N, tokens - nt * N);
       const uint8_t* src = Xs + (size_t)nt * N * G;
       const uint32_t bytes = (uint32_t)(rows * G), bulk = bytes & ~15u;
-      named_sync(1, 128);                      // the four warps are done with the tile before
       if (warp == 6) {
         if (bulk && elect_one()) {
           mbar_expect_tx(rawfull, bulk);
