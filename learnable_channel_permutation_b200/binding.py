@@ -199,6 +199,41 @@ def _enqueue(fn, index: int, *args, stream: Optional[torch.cuda.Stream] = None) 
         check(st)
 
 
+class _Held:
+    """What a prepared object keeps on the device: its own buffers, which belong to the stream that is current when
+    it is made, and the caller's tensors.  ``on(stream)`` comes before a call on that stream (None: the current one)
+    and returns its raw handle.  The first call on a stream other than the object's own waits for the work that was
+    enqueued before the buffers were allocated, which may still use their memory, and tells the allocator of the
+    stream, so that nothing held here is handed out again before the calls have run, even if the object is dropped."""
+
+    def __init__(self, device: torch.device, tensors: Sequence[torch.Tensor]):
+        self.index, self.tensors = device.index, tensors
+        self.known = {torch._C._cuda_getCurrentRawStream(self.index)}
+        self.made = None
+        home = torch.cuda.current_stream(self.index)
+        if not self._capturing(home):
+            self.made = torch.cuda.Event()
+            self.made.record(home)
+
+    def _capturing(self, stream: torch.cuda.Stream) -> bool:
+        if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(self.index) and torch._C._cuda_getDevice() == self.index:
+            return torch._C._cuda_isCurrentStreamCapturing()
+        with torch.cuda.stream(stream):
+            return torch._C._cuda_isCurrentStreamCapturing()
+
+    def on(self, stream: Optional[torch.cuda.Stream]) -> int:
+        raw = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
+        if raw not in self.known:
+            s = torch.cuda.current_stream(self.index) if stream is None else stream
+            for t in self.tensors:
+                t.record_stream(s)
+            if not self._capturing(s):      # a capture cannot wait for work outside it: it begins synchronised
+                if self.made is not None:
+                    s.wait_event(self.made)
+                self.known.add(raw)
+        return raw
+
+
 def hparams(block: int, n: int, m: int, iters: int, tau: float, dtype: int, flags: int = 0) -> LcpHparams:
     return LcpHparams(block, n, m, iters, float(tau), dtype, flags)
 
@@ -238,13 +273,15 @@ class Step:
         if workspace.numel() < self.ws_bytes:
             raise ValueError("workspace too small")
         self.ws = workspace
+        self._held = _Held(workspace.device, [workspace] + [t for d in self.layers for t in d.values()
+                                                            if isinstance(t, torch.Tensor) and t.is_cuda])
         c = _c_int(0)
         check(lib().lcp_step_launches(self.arr, self.n, ctypes.byref(self.hp), ctypes.byref(c)))
         self.launches = int(c.value)
 
     def run(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         check(lib().lcp_step(self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(), self.ws.numel(),
-                             _stream(stream)))
+                             self._held.on(stream)))
 
     def run_timed(self, events: List[torch.cuda.Event], stream: Optional[torch.cuda.Stream] = None) -> None:
         """Stage events of the first layer (TIMED_EVENTS events) or of every
@@ -256,7 +293,7 @@ class Step:
                 raise ValueError("events must be created (record once) before use")
         arr = (_c_void_p * len(events))(*[e.cuda_event for e in events])
         check(lib().lcp_step_timed(self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(), self.ws.numel(),
-                                   _stream(stream), arr, len(events)))
+                                   self._held.on(stream), arr, len(events)))
 
 
 def step_shard(step: "Step", total_tokens: int, dP: Sequence[torch.Tensor], ckpt: Sequence[torch.Tensor],
@@ -269,7 +306,7 @@ def step_shard(step: "Step", total_tokens: int, dP: Sequence[torch.Tensor], ckpt
     dps = (_c_void_p * step.n)(*[_ptr(t, torch.float32, "dP") for t in dP])
     cks = (_c_void_p * step.n)(*[_ptr(t, torch.float32, "ckpt") for t in ckpt])
     check(lib().lcp_step_shard(step.arr, step.n, ctypes.byref(step.hp), int(total_tokens), dps, cks,
-                               step.ws.data_ptr(), step.ws.numel(), _stream(stream)))
+                               step.ws.data_ptr(), step.ws.numel(), step._held.on(stream)))
 
 
 def adamw_params(lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -314,7 +351,7 @@ def _addresses(tensors, dtypes, name: str) -> List[int]:
 class _TensorList:
     """The norm and workspace buffers of a prepared list, allocated once; a call runs on the list's device."""
 
-    def _prepare(self, count: int, device: torch.device) -> None:
+    def _prepare(self, count: int, device: torch.device, tensors: List[torch.Tensor]) -> None:
         nbytes = ctypes.c_size_t(0)
         check(lib().lcp_clip_workspace_size(count, ctypes.byref(nbytes)))
         self.n = count
@@ -323,8 +360,10 @@ class _TensorList:
         self.norm_out = torch.empty(1, dtype=torch.float32, device=device)
         self.tail = (self.norm_out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         self.head = (ctypes.cast(self.arr, ctypes.POINTER(self.arr._type_)), count)
+        self.held = _Held(device, [self.ws, self.norm_out] + tensors)
 
     def _call(self, fn, *args, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+        self.held.on(stream)
         _enqueue(fn, self.device.index, *self.head, *args, *self.tail, stream=stream)
         return self.norm_out
 
@@ -353,7 +392,7 @@ class GradList(_TensorList):
             spans += [(b_, k) for a, b_, k in zip(p, q, size) if a != b_]
         _check_disjoint(spans)
         self.arr = (LcpGrad * max(1, len(p)))(*zip(p, q, n, dt))
-        self._prepare(len(p), device)
+        self._prepare(len(p), device, self.grads if out is None else self.grads + self.out)
 
     def norm(self, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         return self._call(lib().lcp_grad_norm, stream=stream)
@@ -372,7 +411,8 @@ class AdamwList(_TensorList):
         self.tensors = [list(L), list(dL), list(m), list(v)]
         if len({len(x) for x in self.tensors}) != 1:
             raise ValueError("L, dL, m and v must be lists of one length")
-        device = _list_device([t for x in self.tensors for t in x])
+        every = [t for x in self.tensors for t in x]
+        device = _list_device(every)
         n = [t.numel() for t in self.tensors[0]]
         if any([t.numel() for t in x] != n for x in self.tensors[1:]):
             raise ValueError("a parameter, its gradient and its moments have one size")
@@ -380,7 +420,7 @@ class AdamwList(_TensorList):
         size = [4 * k for k in n]
         _check_disjoint([span for p in ptrs for span in zip(p, size)])
         self.arr = (LcpAdamwTensor * max(1, len(n)))(*zip(*ptrs, n))
-        self._prepare(len(n), device)
+        self._prepare(len(n), device, every)
 
     def run(self, opt: LcpAdamwParams, t: int, max_norm: float = float("inf"),
             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
@@ -403,6 +443,7 @@ class Trainer:
         self.state = (LcpAdamwState * len(self.moments))(*[LcpAdamwState(m.data_ptr(), v.data_ptr())
                                                            for m, v in self.moments])
         self.max_norm, self.ws = max_norm, step.ws
+        held = [t for pair in self.moments for t in pair]
         if max_norm is not None:
             _check_disjoint([(t.data_ptr(), 4 * t.numel()) for d in step.layers for t in (d["L"], d["dL"])])
             nbytes = ctypes.c_size_t(0)
@@ -410,18 +451,20 @@ class Trainer:
             self.grad_norm = torch.empty(1, dtype=torch.float32, device=step.ws.device)
             if step.ws.numel() < nbytes.value:
                 self.ws = torch.empty(int(nbytes.value), dtype=torch.uint8, device=step.ws.device)
+            held += [self.grad_norm, self.ws]
+        self._held = _Held(step.ws.device, held)
 
     def run(self, first: int, count: int, stream: Optional[torch.cuda.Stream] = None) -> None:
         s = self.step
+        s._held.on(stream)
+        raw = self._held.on(stream)
         if self.max_norm is not None:
             check(lib().lcp_train_clip(s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count,
                                        self.total, self.tau_start, self.tau_end, float(self.max_norm),
-                                       self.grad_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-                                       _stream(stream)))
+                                       self.grad_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(), raw))
             return
         check(lib().lcp_train(s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count,
-                              self.total, self.tau_start, self.tau_end, s.ws.data_ptr(), s.ws.numel(),
-                              _stream(stream)))
+                              self.total, self.tau_start, self.tau_end, s.ws.data_ptr(), s.ws.numel(), raw))
 
 
 def capture(step: "Step", events: Optional[List[torch.cuda.Event]] = None) -> "torch.cuda.CUDAGraph":
