@@ -8,6 +8,7 @@ library is missing, the first call raises: there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -199,6 +200,19 @@ def _enqueue(fn, index: int, *args, stream: Optional[torch.cuda.Stream] = None) 
         check(st)
 
 
+def _on_device(index: int):
+    """A context in which CUDA device ``index`` is the current one."""
+    return contextlib.nullcontext() if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
+def _clip_workspace(count: int, index: int) -> int:
+    """Bytes of workspace that a list of ``count`` tensors needs on a device."""
+    nbytes = ctypes.c_size_t(0)
+    with _on_device(index):
+        check(lib().lcp_clip_workspace_size(count, ctypes.byref(nbytes)))
+    return int(nbytes.value)
+
+
 class _Held:
     """What a prepared object keeps on the device: its own buffers, which belong to the stream that is current when
     it is made, and the caller's tensors.  ``on(stream)`` comes before a call on that stream (None: the current one)
@@ -280,8 +294,9 @@ class Step:
         self.launches = int(c.value)
 
     def run(self, stream: Optional[torch.cuda.Stream] = None) -> None:
-        check(lib().lcp_step(self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(), self.ws.numel(),
-                             self._held.on(stream)))
+        self._held.on(stream)
+        _enqueue(lib().lcp_step, self._held.index, self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(),
+                 self.ws.numel(), stream=stream)
 
     def run_timed(self, events: List[torch.cuda.Event], stream: Optional[torch.cuda.Stream] = None) -> None:
         """Stage events of the first layer (TIMED_EVENTS events) or of every
@@ -292,8 +307,10 @@ class Step:
             if e.cuda_event == 0:
                 raise ValueError("events must be created (record once) before use")
         arr = (_c_void_p * len(events))(*[e.cuda_event for e in events])
-        check(lib().lcp_step_timed(self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(), self.ws.numel(),
-                                   self._held.on(stream), arr, len(events)))
+        raw = self._held.on(stream)
+        with _on_device(self._held.index):
+            check(lib().lcp_step_timed(self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(), self.ws.numel(),
+                                       raw, arr, len(events)))
 
 
 def step_shard(step: "Step", total_tokens: int, dP: Sequence[torch.Tensor], ckpt: Sequence[torch.Tensor],
@@ -305,8 +322,9 @@ def step_shard(step: "Step", total_tokens: int, dP: Sequence[torch.Tensor], ckpt
         raise ValueError("one dP and one ckpt tensor per layer")
     dps = (_c_void_p * step.n)(*[_ptr(t, torch.float32, "dP") for t in dP])
     cks = (_c_void_p * step.n)(*[_ptr(t, torch.float32, "ckpt") for t in ckpt])
-    check(lib().lcp_step_shard(step.arr, step.n, ctypes.byref(step.hp), int(total_tokens), dps, cks,
-                               step.ws.data_ptr(), step.ws.numel(), step._held.on(stream)))
+    step._held.on(stream)
+    _enqueue(lib().lcp_step_shard, step._held.index, step.arr, step.n, ctypes.byref(step.hp), int(total_tokens), dps, cks,
+             step.ws.data_ptr(), step.ws.numel(), stream=stream)
 
 
 def adamw_params(lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -352,11 +370,9 @@ class _TensorList:
     """The norm and workspace buffers of a prepared list, allocated once; a call runs on the list's device."""
 
     def _prepare(self, count: int, device: torch.device, tensors: List[torch.Tensor]) -> None:
-        nbytes = ctypes.c_size_t(0)
-        check(lib().lcp_clip_workspace_size(count, ctypes.byref(nbytes)))
         self.n = count
         self.device = device
-        self.ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8, device=device)
+        self.ws = torch.empty(max(_clip_workspace(count, device.index), 256), dtype=torch.uint8, device=device)
         self.norm_out = torch.empty(1, dtype=torch.float32, device=device)
         self.tail = (self.norm_out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         self.head = (ctypes.cast(self.arr, ctypes.POINTER(self.arr._type_)), count)
@@ -446,42 +462,42 @@ class Trainer:
         held = [t for pair in self.moments for t in pair]
         if max_norm is not None:
             _check_disjoint([(t.data_ptr(), 4 * t.numel()) for d in step.layers for t in (d["L"], d["dL"])])
-            nbytes = ctypes.c_size_t(0)
-            check(lib().lcp_clip_workspace_size(step.n, ctypes.byref(nbytes)))
+            nbytes = _clip_workspace(step.n, step.ws.device.index)
             self.grad_norm = torch.empty(1, dtype=torch.float32, device=step.ws.device)
-            if step.ws.numel() < nbytes.value:
-                self.ws = torch.empty(int(nbytes.value), dtype=torch.uint8, device=step.ws.device)
+            if step.ws.numel() < nbytes:
+                self.ws = torch.empty(nbytes, dtype=torch.uint8, device=step.ws.device)
             held += [self.grad_norm, self.ws]
         self._held = _Held(step.ws.device, held)
 
     def run(self, first: int, count: int, stream: Optional[torch.cuda.Stream] = None) -> None:
         s = self.step
         s._held.on(stream)
-        raw = self._held.on(stream)
+        self._held.on(stream)
+        args = (s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count, self.total,
+                self.tau_start, self.tau_end)
         if self.max_norm is not None:
-            check(lib().lcp_train_clip(s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count,
-                                       self.total, self.tau_start, self.tau_end, float(self.max_norm),
-                                       self.grad_norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(), raw))
+            _enqueue(lib().lcp_train_clip, self._held.index, *args, float(self.max_norm), self.grad_norm.data_ptr(),
+                     self.ws.data_ptr(), self.ws.numel(), stream=stream)
             return
-        check(lib().lcp_train(s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count,
-                              self.total, self.tau_start, self.tau_end, s.ws.data_ptr(), s.ws.numel(), raw))
+        _enqueue(lib().lcp_train, self._held.index, *args, s.ws.data_ptr(), s.ws.numel(), stream=stream)
 
 
 def capture(step: "Step", events: Optional[List[torch.cuda.Event]] = None) -> "torch.cuda.CUDAGraph":
     """Capture one lcp_step (and, with ``events``, its stage events) into a CUDA
     graph; replaying it re-runs the step on the same buffers with one launch."""
-    side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(side):
-        step.run(side)                     # first call outside capture (one-time set-up)
-    torch.cuda.current_stream().wait_stream(side)
-    torch.cuda.synchronize()
-    g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g):
-        if events is None:
-            step.run()
-        else:
-            step.run_timed(events)
+    with _on_device(step._held.index):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step.run(side)                     # first call outside capture (one-time set-up)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if events is None:
+                step.run()
+            else:
+                step.run_timed(events)
     return g
 
 
