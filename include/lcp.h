@@ -275,7 +275,7 @@ LCP_API lcp_status lcp_adamw_list(const lcp_adamw_tensor* tensors, int count, co
 /* ("Implementation details") lcp_train with the gradients of all layers clipped together: each
  * step ends with one lcp_adamw_list over the layers' logits instead of an
  * lcp_adamw a layer.  norm[0] receives the last step's norm over all dL (before
- * clipping; dL holds the unclipped gradients).  ws: at least the larger of
+ * clipping; dL holds the unclipped gradients; 0 without layers).  ws: at least the larger of
  * lcp_workspace_size() and lcp_clip_workspace_size(nlayers). */
 LCP_API lcp_status lcp_train_clip(const lcp_layer* layers, int nlayers, const lcp_hparams* hp,
                                   const lcp_adamw_params* opt, const lcp_adamw_state* state, int first, int count,

@@ -668,7 +668,11 @@ static lcp_status train_impl(const lcp_layer* layers, int nlayers, const lcp_hpa
     h.tau = (float)((double)tau_start + ((double)tau_end - (double)tau_start) * frac);
     LCP_TRY(step_impl(layers, nlayers, &h, ws, ws_bytes, stream, nullptr, 0));
     // the partial sums of the norm lie in the step's workspace: the step's kernels are done with it by then
-    if (clip && nlayers > 0)
+    if (clip && nlayers == 0) {      // step_impl launches nothing then and has not asked for the device; the norm is 0
+      LCP_TRY(check_arch());
+      LCP_TRY(check_pending());
+    }
+    if (clip)
       LCP_TRY(launch_adamw_list(list.data(), nlayers, *opt, s + 1, max_norm, norm, ws, stream));
     for (int i = 0; i < nlayers && !clip; ++i) {
       const long long n = (long long)layers[i].cin * h.block;
