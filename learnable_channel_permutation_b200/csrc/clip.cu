@@ -95,7 +95,9 @@ __device__ __forceinline__ double sq(float x) { return (double)x * (double)x; }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int NTHR, typename T> __device__ __forceinline__ double chunk_squares(const T* p, int n, bool stream) {
+// CONST: the launch does not write the gradients, so they may be read on the read-only path (norm of
+// 262144 values 2.7 us, 2.8 without).
+template <int NTHR, bool CONST, typename T> __device__ __forceinline__ double chunk_squares(const T* p, int n, bool stream) {
   constexpr int V = 16 / sizeof(T);
   double s0 = 0.0, s1 = 0.0;
   int head = head_of<sizeof(T)>(p);
@@ -104,7 +106,7 @@ template <int NTHR, typename T> __device__ __forceinline__ double chunk_squares(
   const uint4* q = reinterpret_cast<const uint4*>(p + head);
 #pragma unroll 4
   for (int i = threadIdx.x; i < vecs; i += NTHR) {
-    const uint4 u = stream ? __ldcs(q + i) : __ldg(q + i);
+    const uint4 u = stream ? __ldcs(q + i) : CONST ? __ldg(q + i) : q[i];
     if constexpr (sizeof(T) == 4) {
       s0 += sq(__uint_as_float(u.x)) + sq(__uint_as_float(u.y));
       s1 += sq(__uint_as_float(u.z)) + sq(__uint_as_float(u.w));
@@ -140,9 +142,10 @@ template <typename Table> __device__ __forceinline__ bool is_bf16(const Table& t
   if constexpr (is_adam<Table>::value) return false;
   else return t.bf16[i];
 }
-template <int NTHR, typename Table> __device__ __forceinline__ double squares_of(const Table& t, const ChunkAt& a, bool stream) {
-  if (is_bf16(t, a.i)) return chunk_squares<NTHR>(reinterpret_cast<const __nv_bfloat16*>(t.g[a.i]) + a.at, a.n, stream);
-  return chunk_squares<NTHR>(reinterpret_cast<const float*>(t.g[a.i]) + a.at, a.n, stream);
+template <int NTHR, bool CONST, typename Table>
+__device__ __forceinline__ double squares_of(const Table& t, const ChunkAt& a, bool stream) {
+  if (is_bf16(t, a.i)) return chunk_squares<NTHR, CONST>(reinterpret_cast<const __nv_bfloat16*>(t.g[a.i]) + a.at, a.n, stream);
+  return chunk_squares<NTHR, CONST>(reinterpret_cast<const float*>(t.g[a.i]) + a.at, a.n, stream);
 }
 
 template <int CHUNK, typename Table>
@@ -154,7 +157,7 @@ squares_kernel(const __grid_constant__ Table t, double* __restrict__ partials, l
   const int chunks = t.first[t.count];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const ChunkAt a = chunk_at<CHUNK>(t, c);
-    s += squares_of<kThreads>(t, a, (long long)(chunks - c) * CHUNK * (is_bf16(t, a.i) ? 2 : 4) > keep);
+    s += squares_of<kThreads, true>(t, a, (long long)(chunks - c) * CHUNK * (is_bf16(t, a.i) ? 2 : 4) > keep);
   }
   s = block_sum<kThreads>(s);
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
@@ -297,7 +300,7 @@ small_kernel(const __grid_constant__ Table t, double max_norm, float* __restrict
   double s = 0.0;
   if (rank < t.first[t.count]) {
     a = chunk_at<kSmallChunk>(t, rank);
-    s = squares_of<kSmallThreads>(t, a, false);
+    s = squares_of<kSmallThreads, !APPLY>(t, a, false);      // clipped in place further down
   }
   s = block_sum<kSmallThreads>(s);
   if (threadIdx.x == 0) mine = s;
