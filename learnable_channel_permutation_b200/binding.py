@@ -189,13 +189,13 @@ def _arg(t: Optional[torch.Tensor], dtype, index: int, name: str) -> Optional[in
     return t.data_ptr()
 
 
-def _enqueue(fn, index: int, *args, stream: Optional[torch.cuda.Stream] = None) -> None:
-    """Calls ``fn(*args, stream)`` with CUDA device ``index`` current, on its current stream unless one is given (the
-    raw handle: a Stream object costs as much as a launch)."""
+def _enqueue(fn, index: int, *args, raw: Optional[int] = None) -> None:
+    """Calls ``fn(*args, stream)`` with CUDA device ``index`` current, on its current stream unless one is given (by
+    its raw handle: a Stream object costs as much as a launch)."""
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return _enqueue(fn, index, *args, stream=stream)
-    st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+            return _enqueue(fn, index, *args, raw=raw)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if raw is None else raw)
     if st:
         check(st)
 
@@ -237,7 +237,7 @@ class _Held:
 
     def on(self, stream: Optional[torch.cuda.Stream]) -> int:
         raw = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
-        if raw not in self.known:
+        if raw not in self.known:       # rare: a call on a known stream costs a look-up
             s = torch.cuda.current_stream(self.index) if stream is None else stream
             for t in self.tensors:
                 t.record_stream(s)
@@ -294,9 +294,9 @@ class Step:
         self.launches = int(c.value)
 
     def run(self, stream: Optional[torch.cuda.Stream] = None) -> None:
-        self._held.on(stream)
+        raw = self._held.on(stream)
         _enqueue(lib().lcp_step, self._held.index, self.arr, self.n, ctypes.byref(self.hp), self.ws.data_ptr(),
-                 self.ws.numel(), stream=stream)
+                 self.ws.numel(), raw=raw)
 
     def run_timed(self, events: List[torch.cuda.Event], stream: Optional[torch.cuda.Stream] = None) -> None:
         """Stage events of the first layer (TIMED_EVENTS events) or of every
@@ -322,9 +322,9 @@ def step_shard(step: "Step", total_tokens: int, dP: Sequence[torch.Tensor], ckpt
         raise ValueError("one dP and one ckpt tensor per layer")
     dps = (_c_void_p * step.n)(*[_ptr(t, torch.float32, "dP") for t in dP])
     cks = (_c_void_p * step.n)(*[_ptr(t, torch.float32, "ckpt") for t in ckpt])
-    step._held.on(stream)
+    raw = step._held.on(stream)
     _enqueue(lib().lcp_step_shard, step._held.index, step.arr, step.n, ctypes.byref(step.hp), int(total_tokens), dps, cks,
-             step.ws.data_ptr(), step.ws.numel(), stream=stream)
+             step.ws.data_ptr(), step.ws.numel(), raw=raw)
 
 
 def adamw_params(lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -379,8 +379,8 @@ class _TensorList:
         self.held = _Held(device, [self.ws, self.norm_out] + tensors)
 
     def _call(self, fn, *args, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-        self.held.on(stream)
-        _enqueue(fn, self.device.index, *self.head, *args, *self.tail, stream=stream)
+        raw = self.held.on(stream)
+        _enqueue(fn, self.device.index, *self.head, *args, *self.tail, raw=raw)
         return self.norm_out
 
 
@@ -472,14 +472,14 @@ class Trainer:
     def run(self, first: int, count: int, stream: Optional[torch.cuda.Stream] = None) -> None:
         s = self.step
         s._held.on(stream)
-        self._held.on(stream)
+        raw = self._held.on(stream)
         args = (s.arr, s.n, ctypes.byref(s.hp), ctypes.byref(self.opt), self.state, first, count, self.total,
                 self.tau_start, self.tau_end)
         if self.max_norm is not None:
             _enqueue(lib().lcp_train_clip, self._held.index, *args, float(self.max_norm), self.grad_norm.data_ptr(),
-                     self.ws.data_ptr(), self.ws.numel(), stream=stream)
+                     self.ws.data_ptr(), self.ws.numel(), raw=raw)
             return
-        _enqueue(lib().lcp_train, self._held.index, *args, s.ws.data_ptr(), s.ws.numel(), stream=stream)
+        _enqueue(lib().lcp_train, self._held.index, *args, s.ws.data_ptr(), s.ws.numel(), raw=raw)
 
 
 def capture(step: "Step", events: Optional[List[torch.cuda.Event]] = None) -> "torch.cuda.CUDAGraph":
