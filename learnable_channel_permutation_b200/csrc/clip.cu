@@ -486,9 +486,11 @@ template <bool APPLY, template <int> class T, typename Desc>
 lcp_status run_list(const Desc* d, int count, double max_norm, float* norm, void* ws, const AdamCoef& c, cudaStream_t st,
                     const char* what) {
   static thread_local T<kCapLarge> t;       // 28 KB: off the caller's stack
-  // Short lists take one launch of one cluster: up to 65536 values clipped in 5.5 us, 7.2 with two launches;
-  // from there on the cluster's 16 SMs are the slower way (262144 values: 7.3 us, and 10.8 for the
-  // update, against 4.5 and 5.5).
+  // Short lists take one launch of one cluster, for a launch less on the host.  One call after another from
+  // the host, clipping and update, one launch and two: 4096 values 4.3 / 6.1 and 4.8 / 6.4 us, 65536 values 5.6 / 6.1
+  // and 6.5 / 6.4, which is the border.  In a captured graph, where that launch costs less, two are ahead from some
+  // 32768 values on: 4096 values 2.9 / 3.9 and 4.2 / 4.4 us, 32768 3.9 / 4.0 and 5.0 / 4.5, 65536 5.4 / 3.9 and
+  // 6.3 / 4.6.
   long long small = 0;
   for (int i = 0; i < count && small <= kSmallCluster; ++i) small += chunks_of(d[i].n, kSmallChunk);
   if (small > 0 && small <= kSmallCluster) {

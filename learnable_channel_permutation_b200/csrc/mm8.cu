@@ -115,12 +115,26 @@ __device__ __forceinline__ void wait_through_cluster(uint32_t bar, uint32_t pari
 constexpr int M8_BM = 128;            // output channels of a CTA: one row of weight scales
 constexpr int M8_A = M8_BM * 128;     // bytes of a stage's weight tile (one scale group of channels)
 constexpr int M8_SF = 4;              // ring of scale chunks (four groups each)
+constexpr int M8_MAX_STAGES = 12;
+constexpr int M8_RING = 210 * 1024, M8_HALF_RING = 96 * 1024;      // bytes of the operand ring: one CTA an SM, two
 constexpr int M8_FUSED_TOKENS = 8;    // plain activations of up to so many tokens are quantised by the product itself
                                       // (8 tokens x 4096 x 11008: 12.3 us; 16: 17.0, 13.2 as two launches)
 constexpr int M8_FUSED_WARPS = 8;     // warps that do (16 leave one CTA an SM: 16.2 us, 6.9 then, at 4096 x 4096)
+// Every how many pairs of groups a quantising warp takes, where warps go round npp pairs of tokens and a ring
+// of `stages` tiles.
+__host__ __device__ constexpr int fused_every(int stages, int npp) {
+  int every = M8_FUSED_WARPS / npp;
+  while (2 * every > stages) every /= 2;
+  return every;
+}
+constexpr bool fused_ring_ok(int bytes) {      // for one pair of tokens, where `every` is largest
+  const int stages = bytes / (M8_A + 16 * 128);
+  return stages <= M8_MAX_STAGES && 2 * fused_every(stages, 1) + stages <= 19;
+}
+static_assert(M8_FUSED_TOKENS <= 16 && fused_ring_ok(M8_RING) && fused_ring_ok(M8_HALF_RING),
+              "an arrival for a missing pair of groups could fall into an older phase");
 // warp 0: TMA, 1: MMA, 2-5: epilogue; 6: scales, or all from 2 on: quantisers
 template <typename XT> constexpr int m8_threads() { return sizeof(XT) == 1 ? 224 : 64 + 32 * M8_FUSED_WARPS; }
-constexpr int M8_MAX_STAGES = 12;
 constexpr int M8_SETS = 4;            // sets of scales in tensor memory
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
@@ -319,13 +333,16 @@ mm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       // share a pair of tokens, and no more than stages / 2: a warp that waits for a tile knows from its
       // own wait before, 2 every groups back, that the tile's use before the last is over, so the parity
       // it waits for cannot be an older phase's.
+      // A last chunk of one or two groups lacks its second pair, whose warp arrives on sffull without a wait.
+      // That must not fall into the phase before, of chunk c - 4: the warp's own last wait, for the tile of group
+      // 4 c + 3 - 2 every, says that the products of `stages` groups earlier are done, and so the words of their
+      // chunk complete.  They are no earlier than chunk c - 4 where 2 every + stages <= 19 (asserted at fused_every).
       pdl_wait();
       const int w = warp - 2;
       int npp = 1;
       while (npp < npairs) npp *= 2;
       const int pair = w % npp;
-      int every = M8_FUSED_WARPS / npp;
-      while (2 * every > stages) every /= 2;
+      const int every = fused_every(stages, npp);
       uint32_t* buf = exchange + (PERM ? w * Q8_STAGE : 0);
       const int row0 = 2 * pair;
       auto load = [&](int p, int u) {
@@ -792,7 +809,7 @@ lcp_status split_t(const XT* X, const int32_t* perm, int B, const uint8_t* Xs, c
   if (sizeof(XT) == 1) TC_TRY(make_map8(&mX, X, cin, tokens, p.NT, "mm8 X"));
   else mX = mW;      // not used
   const int stage_bytes = M8_A + p.NT * 128;
-  int stages = (p.per_sm == 2 ? 96 * 1024 : 210 * 1024) / stage_bytes;
+  int stages = (p.per_sm == 2 ? M8_HALF_RING : M8_RING) / stage_bytes;
   if (stages > M8_MAX_STAGES) stages = M8_MAX_STAGES;
   const int smem = stages * stage_bytes + M8_SF * 1024 + (PERM ? M8_FUSED_WARPS * Q8_STAGE * 4 : 0) + 1024 + 512;
   const auto kernel = mm8_split_kernel<OUT, XT, PERM>;
