@@ -429,7 +429,8 @@ LCP_API lcp_status lcp_sparse24_mm(const void* values, const uint32_t* meta, con
  *
  * Quantisation: with amax the largest magnitude of a block, its scale is 2^k, k
  * the smallest integer >= -127 with amax <= 448 2^k (k = 0 for a block of
- * zeros), and q = x 2^-k rounded to the nearest e4m3 value, ties to even.  A
+ * zeros), and q = x 2^-k rounded to the nearest e4m3 value, ties to even (off by at
+ * most 2^-4 of the value, or 2^-10 of the scale where that is more).  A
  * block that holds an infinity or a NaN gets the NaN scale and NaN values, and
  * so does every output it enters.
  *
@@ -452,8 +453,9 @@ LCP_API lcp_status lcp_quant8_weight(const void* W, const int32_t* perm, const u
                                      int cout, int cin, int B, lcp_dtype dtype, cudaStream_t stream);
 
 /* ("Effect on inference acceleration": the deployed product) Y [T, C_out] = X W^T of 8-bit operands, Xq [T, C_in] with
- * Xs [T, G] and Wq [C_out, C_in] with Ws [ceil(C_out/128), G]; products and sums in float32 on the tensor cores, Y
- * rounded to `ydtype` once.  T = 0 is a no-op. */
+ * Xs [T, G] and Wq [C_out, C_in] with Ws [ceil(C_out/128), G]; products and sums in float32 on the tensor cores, whose
+ * additions may truncate: before Y is rounded to `ydtype` (once) an output is within (C_in/32 + 40) 2^-23 of the sum of
+ * its terms' magnitudes.  T = 0 is a no-op. */
 LCP_API lcp_status lcp_mm8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws, void* Y, int cout,
                            int cin, int tokens, lcp_dtype ydtype, cudaStream_t stream);
 

@@ -21,7 +21,9 @@
 // The second pass walks the chunks backwards: the end of the list is what the
 // first pass left in L2.  Everything but those kKeep bytes is read and written
 // with streaming accesses, so that it stays there (a 7B model's logits, 291 MB:
-// 143 us without, 138 with 64 to 80 MB kept, 140 with 112).
+// 143 us without, 138 with 64 to 80 MB kept, 140 with 112).  That is one table of
+// kCapLarge tensors: a longer list takes each pass table by table, front first,
+// every table with an end of its own, and little of what is left in L2 is met again.
 
 #include <algorithm>
 #include <atomic>

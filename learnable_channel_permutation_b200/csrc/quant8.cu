@@ -7,8 +7,10 @@
 // The scale of a block with largest magnitude amax is 2^k, k the smallest
 // integer >= -127 with amax <= 448 2^k (448 is e4m3's largest value; k = 0 for a
 // block of zeros), and a value becomes q = rn_e4m3(x 2^-k).  The product x 2^-k
-// only moves the exponent, so the rounding to e4m3 (to nearest, ties to even;
-// at most half a step, 2^-4 of the value) is the only one made.  A block that
+// only moves the exponent, so the rounding to e4m3 (to nearest, ties to even) is
+// the only one made.  It is at most half a step: 2^-4 of the value, or 2^-10 of
+// the scale where that is more (values under 2^-6 of the scale, which e4m3 holds
+// as subnormals; under 2^-10 of it they become zero).  A block that
 // holds an infinity or a NaN gets the NaN scale (0xff) and NaN values, so every
 // product it enters is NaN.
 //
